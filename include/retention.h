@@ -462,6 +462,129 @@ ret_status ret_linear_bf16(const void* X, const void* W, void* Y, int M, int N, 
                            cudaStream_t stream);
 
 /*
+ * Rotary positions on q and k, of any layout, on part of the head, at
+ * positions per token.  Pair p of a row at position n is turned by n freqs[p]
+ * and multiplied by scale:
+ *     [a', b'] = scale [a cos - b sin, a sin + b cos];
+ * layout RET_ROTARY_INTERLEAVED: the pair is (2p, 2p+1) (ret_xpos_rotate's);
+ * RET_ROTARY_HALF: (p, p + rotary_dim/2).  The components from rotary_dim on
+ * are copied.  inverse != 0 turns by -n freqs[p] instead (the factor stays):
+ * the transpose, i.e. the gradient of the call without it.
+ * q, k: device [B, N, H, d] and [B, N, Hk, d] of dtype dt; k NULL: q alone.
+ * q_out, k_out: the same shapes.  Each *_strides: host pointer to the element
+ * strides of batch, token and head (components consecutive), or NULL
+ * (contiguous).  An output may be its own input (same pointer and strides);
+ * any other overlap of an output is RET_ERR_INVALID_ARG, except that views
+ * with the same batch and token strides may interleave by whole rows (q and k
+ * of one fused projection).
+ * freqs: host, rotary_dim/2 finite doubles (ret_rotary_frequencies).
+ * positions: device int64 [B, N], or NULL: token n of every sequence is at
+ * pos_offset + n.  Angles are 64-bit products, so far positions keep theirs.
+ * rotary_dim even, 2 <= rotary_dim <= min(d, 512); d even; fewer than 2^31
+ * tokens.
+ */
+#define RET_ROTARY_INTERLEAVED 0
+#define RET_ROTARY_HALF 1
+
+ret_status ret_rotary(const void* q, const void* k, void* q_out, void* k_out, const int64_t* q_strides,
+                      const int64_t* k_strides, const int64_t* q_out_strides, const int64_t* k_out_strides,
+                      const double* freqs, double scale, const int64_t* positions, int64_t pos_offset, int inverse,
+                      int layout, int B, int N, int H, int Hk, int d, int rotary_dim, ret_dtype dt,
+                      cudaStream_t stream);
+
+/*
+ * Host helper: the angles per position of ret_rotary and the factor on cos
+ * and sin.  Plain: f_p = theta_base^(-2p/rotary_dim), factor 1.  With f =
+ * `factor` >= 1, the stretch of the context:
+ *   RET_ROTARY_LINEAR  every angle divided by f (position interpolation);
+ *   RET_ROTARY_YARN    by parts: pairs that turn more than beta_fast times
+ *     over original_length tokens keep their angle, those that turn fewer than
+ *     beta_slow times get it divided by f, a linear ramp over the pair index
+ *     between; the factor on cos and sin is 0.1 ln f + 1.
+ * freqs: host, rotary_dim/2 doubles, written; scale: host, written.
+ */
+#define RET_ROTARY_PLAIN 0
+#define RET_ROTARY_LINEAR 1
+#define RET_ROTARY_YARN 2
+
+ret_status ret_rotary_frequencies(int rotary_dim, double theta_base, int scaling, double factor,
+                                  double original_length, double beta_fast, double beta_slow, double* freqs,
+                                  double* scale);
+
+/*
+ * Layer norm of `rows` rows of d components (the norm of ret_retnet_block_forward
+ * on its own, with the statistics its gradient needs):
+ *     y = (x - mean) rstd gain + bias,  rstd = 1 / sqrt(var + eps)  (biased variance).
+ * x, y: device [rows, d] of dtype dt; gain, bias: device [d] of dtype w_dt, or
+ * NULL (1, 0); mean, rstd: device fp32 [rows], written, or NULL.
+ * The backward computes, for dy = dL/dy and the forward's mean and rstd, with
+ * h = (x - mean) rstd and t = dy gain,
+ *     dx = rstd (t - avg(t) - h avg(t h)),  dgain = sum_rows dy h,  dbias = sum_rows dy
+ * (averages over the row): dx of dtype dt, dgain and dbias fp32 [d]; each may be
+ * NULL.  The sums over the rows are added in a fixed order: a call on the same
+ * inputs gives the same bits.  They need a workspace (device, 256-byte aligned,
+ * overlapping nothing) of ret_layernorm_backward_workspace_bytes(rows, d) bytes
+ * when dgain or dbias is given.
+ * 1 <= d <= 8192 (else RET_ERR_UNSUPPORTED).  Pointers aligned to their
+ * element; rows of a multiple of 16 bytes at 16-byte aligned pointers are read
+ * in vectors.  No output overlaps another buffer.
+ */
+ret_status ret_layernorm_forward(const void* x, const void* gain, const void* bias, double eps, int64_t rows, int d,
+                                 void* y, float* mean, float* rstd, ret_dtype dt, ret_dtype w_dt,
+                                 cudaStream_t stream);
+
+size_t ret_layernorm_backward_workspace_bytes(int64_t rows, int d);
+
+ret_status ret_layernorm_backward(const void* dy, const void* x, const float* mean, const float* rstd,
+                                  const void* gain, int64_t rows, int d, void* dx, float* dgain, float* dbias,
+                                  ret_dtype dt, ret_dtype w_dt, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream);
+
+/*
+ * The gated delta rule: a state that decays by a factor per token and
+ * corrects what it holds for the token's key,
+ *     S' = exp(g_t) S_{t-1},  u_t = beta_t (v_t - S'^T k_t),
+ *     S_t = S' + k_t u_t^T,   o_t = S_t^T q_t.
+ * (Retention is the same with a fixed decay and u_t = v_t.)
+ * Layout: q, k [B, N, Hk, dk]; v, out [B, N, H, dv]; g, beta [B, N, H] fp32;
+ * states [B, H, dk, dv] fp32; H a multiple of Hk, value head h reads key head
+ * h / (H / Hk).  g is the logarithm of the decay, g <= 0 (-inf: the state is
+ * dropped); the rule is stable for beta |k|^2 in [0, 2].  Scaling of q and
+ * normalising of k are the caller's.  dk <= 256.  q, k, v, out and the states
+ * 16-byte aligned, g, beta and lengths 4-byte aligned.
+ * lengths: device int32 [B], or NULL: sequence b has lengths[b] tokens
+ * (clamped to [0, N]); the rows behind them are neither read into the result
+ * (whatever they hold) nor written in out, and the final state is the state
+ * after lengths[b] tokens.
+ *
+ * ret_delta_forward_chunkwise
+ *   initial_state, final_state: or NULL (zero; not wanted); they may be the
+ *   same buffer.  A sequence split into calls that hand the state on gives
+ *   the single call's result up to rounding.
+ *   bf16 inputs with dk 64, 128 or 256 and dv a multiple of 8 run in chunks of
+ *   64 tokens on the tensor cores; bf16 rounding errors of the state, of the
+ *   corrections u and of the scores are carried as a second bf16 term, so the
+ *   result is that of fp32 arithmetic on the given inputs.  They need a
+ *   workspace (device, 256-byte aligned, overlapping nothing, scratch) of
+ *   ret_delta_workspace_bytes(...) bytes.  Other shapes (fp32, other dk or dv)
+ *   run token by token on the CUDA cores; the size is 0 for them.
+ *
+ * ret_delta_decode_step: one token; q, k [B, Hk, dk], v, out [B, H, dv],
+ *   g, beta [B, H], state updated in place, dv a multiple of 4.
+ */
+size_t ret_delta_workspace_bytes(int B, int N, int Hk, int H, int dk, int dv, ret_dtype in_dt);
+
+ret_status ret_delta_forward_chunkwise(const void* q, const void* k, const void* v, const float* g,
+                                       const float* beta, const int32_t* lengths, const float* initial_state, int B,
+                                       int N, int Hk, int H, int dk, int dv, void* out, float* final_state,
+                                       cudaStream_t stream, ret_dtype in_dt, ret_dtype out_dt, void* workspace,
+                                       size_t workspace_bytes);
+
+ret_status ret_delta_decode_step(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                                 float* state, void* out, cudaStream_t stream, int B, int Hk, int H, int dk, int dv,
+                                 ret_dtype in_dt, ret_dtype out_dt);
+
+/*
  * Diagnostics: one device thread waits on a barrier that nothing arrives on,
  * with the same bounded wait as the tensor-core kernels, for `polls` polls
  * (1 .. 2^24), gives up and sets the device error word.  The following

@@ -28,6 +28,9 @@ __all__ = [
     "NORM_DECAY", "NORM_SCORE",
     "ret_linear_bf16", "ret_retnet_block_forward", "ret_retnet_block_workspace_bytes",
     "ret_forward_parallel", "ret_forward_recurrent", "ret_check_device_error", "ret_last_error_string",
+    "ret_rotary", "ret_rotary_frequencies", "ret_layernorm_forward", "ret_layernorm_backward",
+    "ret_layernorm_backward_workspace_bytes",
+    "ret_delta_forward_chunkwise", "ret_delta_workspace_bytes", "ret_delta_decode_step",
     "RET_OK", "RET_ERR_INVALID_ARG", "RET_ERR_UNSUPPORTED", "RET_ERR_CUDA", "RET_ERR_TIMEOUT",
     "RET_F32", "RET_BF16",
 ]
@@ -92,6 +95,16 @@ def _load_library():
     L.ret_retnet_block_workspace_bytes.restype = ctypes.c_size_t
     L.ret_retnet_block_forward.argtypes = [vp] * 12 + [dp, i, i, i, i, i, i, i, i, d, d, d, i, i64, d, vp, i, vp,
                                                        ctypes.c_size_t, vp]
+    L.ret_rotary_frequencies.argtypes = [i, d, i, d, d, d, d, vp, dp]
+    L.ret_rotary.argtypes = [vp] * 8 + [vp, d, vp, i64, i, i, i, i, i, i, i, i, i, vp]
+    L.ret_layernorm_forward.argtypes = [vp, vp, vp, d, i64, i, vp, vp, vp, i, i, vp]
+    L.ret_layernorm_backward_workspace_bytes.argtypes = [i64, i]
+    L.ret_layernorm_backward_workspace_bytes.restype = ctypes.c_size_t
+    L.ret_layernorm_backward.argtypes = [vp, vp, vp, vp, vp, i64, i, vp, vp, vp, i, i, vp, ctypes.c_size_t, vp]
+    L.ret_delta_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+    L.ret_delta_workspace_bytes.restype = ctypes.c_size_t
+    L.ret_delta_forward_chunkwise.argtypes = [vp] * 7 + [i] * 6 + [vp, vp, vp, i, i, vp, ctypes.c_size_t]
+    L.ret_delta_decode_step.argtypes = [vp] * 8 + [i] * 7
     L.ret_check_device_error.argtypes = [vp]
     L.ret_last_error_string.restype = ctypes.c_char_p
     L.ret_last_error_string.argtypes = []
@@ -577,4 +590,231 @@ def ret_msr_forward(x, wq, wk, wv, wg, wo, gammas, H: int, chunk: int = 128, k_s
                                _ptr(wo, "wo"), _gammas(gammas, H), B, N, dm, H, dk, dv, int(chunk), float(k_scale),
                                float(eps), int(bool(xpos)), int(pos_offset), float(theta_base), _ptr(out, "out"),
                                _dt(out.dtype), _ptr(workspace, "workspace"), nbytes, _stream(stream)))
+    return out
+
+
+# ------------------------------------------------- rotary, layer norm, delta rule
+
+def _call(like: torch.Tensor, stream, fn, *args):
+    """Call ``fn(*args)`` with ``like``'s device current; the argument
+    ``_STREAM`` stands for the stream (default: that device's current one)."""
+    if not like.is_cuda:
+        raise ValueError("the inputs must be CUDA tensors")
+    dev = like.device.index
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    s = _stream(stream)
+    args = [s if a is _STREAM else a for a in args]
+    if dev == torch.cuda.current_device():
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args))
+
+
+_STREAM = object()
+
+_ROTARY_LAYOUTS = {"interleaved": 0, "half": 1}
+_ROTARY_SCALINGS = {"none": 0, "linear": 1, "yarn": 2}
+
+
+def ret_rotary_frequencies(rotary_dim: int, theta_base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                           original_length: float = 4096.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(freqs, scale) for ret_rotary: the angle per position of each pair
+    (float64 [rotary_dim / 2] on the CPU) and the factor on cos and sin, plain
+    or stretched for longer contexts (``scaling`` "none", "linear", "yarn")."""
+    if scaling not in _ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_ROTARY_SCALINGS)} (got {scaling!r})")
+    freqs = torch.empty(max(int(rotary_dim), 2) // 2, dtype=torch.float64)
+    scale = ctypes.c_double()
+    _check(lib.ret_rotary_frequencies(int(rotary_dim), float(theta_base), _ROTARY_SCALINGS[scaling], float(factor),
+                                      float(original_length), float(beta_fast), float(beta_slow),
+                                      ctypes.c_void_p(freqs.data_ptr()), ctypes.byref(scale)))
+    return freqs, scale.value
+
+
+def _rotary_view(t: Optional[torch.Tensor], name: str):
+    """(pointer, strides) of a [B, N, heads, d] view with consecutive components."""
+    if t is None:
+        return None, None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.stride(3) != 1 and t.shape[3] > 1:
+        raise ValueError(f"the components of {name} must be consecutive (stride {t.stride(3)})")
+    return ctypes.c_void_p(t.data_ptr()), (ctypes.c_int64 * 3)(*t.stride()[:3])
+
+
+def ret_rotary(q, k=None, freqs=None, positions=None, pos_offset: int = 0, layout: str = "interleaved",
+               scale: float = 1.0, rotary_dim: Optional[int] = None, theta_base: float = 10000.0, inverse: bool = False,
+               q_out=None, k_out=None, stream=None):
+    """Rotary positions on q [B, N, H, d] and k [B, N, Hk, d] (or None):
+    ``freqs`` from ret_rotary_frequencies (its length sets the turned part of
+    the head), or None for the plain ones of ``rotary_dim`` (default d) and
+    ``theta_base``; ``positions`` int64 [B, N] on the device, or token n at
+    pos_offset + n; layout "interleaved" or "half".  Views with consecutive
+    components are taken as they are; pass ``q_out=q`` to work in place.
+    ``inverse=True`` is the transpose (the gradient).  Returns the output, or
+    the pair of them."""
+    if layout not in _ROTARY_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_ROTARY_LAYOUTS)} (got {layout!r})")
+    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3])):
+        raise ValueError("expected q [B, N, H, d] and k [B, N, Hk, d]")
+    if k is not None and k.dtype != q.dtype:
+        raise TypeError("q and k must share a dtype")
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    B, N, H, d = q.shape
+    Hk = k.shape[2] if k is not None else 0
+    if freqs is None:
+        freqs, _ = ret_rotary_frequencies(d if rotary_dim is None else rotary_dim, theta_base)
+    elif not isinstance(freqs, torch.Tensor):
+        freqs = torch.tensor([float(f) for f in freqs], dtype=torch.float64)
+    if freqs.dim() != 1 or freqs.dtype != torch.float64 or freqs.is_cuda or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous float64 vector on the CPU")
+    if rotary_dim is not None and 2 * freqs.numel() != rotary_dim:
+        raise ValueError(f"freqs has {freqs.numel()} entries, expected {rotary_dim // 2}")
+    q_out = torch.empty((B, N, H, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
+    if k is not None and k_out is None:
+        k_out = torch.empty((B, N, Hk, d), dtype=q.dtype, device=q.device)
+    _buf(q_out, "q_out", (B, N, H, d), (q.dtype,), q)
+    _buf(k_out, "k_out", (B, N, Hk, d), (q.dtype,), q)
+    _buf(positions, "positions", (B, N), (torch.int64,), q)
+    _same_device(q, k=k)
+    (qp, qs), (kp, ks) = _rotary_view(q, "q"), _rotary_view(k, "k")
+    (qop, qos), (kop, kos) = _rotary_view(q_out, "q_out"), _rotary_view(k_out, "k_out")
+    _call(q, stream, lib.ret_rotary, qp, kp, qop, kop, qs, ks, qos, kos, ctypes.c_void_p(freqs.data_ptr()),
+          float(scale), _ptr(positions, "positions"), int(pos_offset), int(bool(inverse)), _ROTARY_LAYOUTS[layout],
+          B, N, H, Hk, d, 2 * freqs.numel(), _dt(q.dtype), _STREAM)
+    return q_out if k is None else (q_out, k_out)
+
+
+def _weight_dt(x, d, **weights):
+    """dtype code of the layer norm's weights (fp32 or bf16, the same for all)."""
+    given = [t for t in weights.values() if t is not None]
+    for name, t in weights.items():
+        _buf(t, name, (d,), FLOATS, x)
+    if any(t.dtype != given[0].dtype for t in given):
+        raise TypeError("gain and bias must share a dtype")
+    return _dt(given[0].dtype) if given else RET_F32
+
+
+def ret_layernorm_forward(x, gain=None, bias=None, eps: float = 1e-5, out=None, mean=None, rstd=None,
+                          want_stats: bool = False, stream=None):
+    """Layer norm over the last dimension of x [..., d]; gain, bias [d] or None.
+    Returns the output, or (out, mean, rstd) (fp32, one per row) when the
+    statistics are passed in or wanted."""
+    if x.dim() < 1 or x.numel() == 0:
+        raise ValueError("x must be [..., d] with at least one row")
+    d, lead = x.shape[-1], x.shape[:-1]
+    rows = x.numel() // d
+    w = _weight_dt(x, d, gain=gain, bias=bias)
+    out = torch.empty_like(x) if out is None else out
+    if want_stats:
+        mean = torch.empty(lead, dtype=torch.float32, device=x.device) if mean is None else mean
+        rstd = torch.empty(lead, dtype=torch.float32, device=x.device) if rstd is None else rstd
+    _buf(out, "out", x.shape, (x.dtype,), x)
+    _buf(mean, "mean", lead, F32, x)
+    _buf(rstd, "rstd", lead, F32, x)
+    _call(x, stream, lib.ret_layernorm_forward, _ptr(x, "x"), _ptr(gain, "gain"), _ptr(bias, "bias"), float(eps), rows,
+          d, _ptr(out, "out"), _ptr(mean, "mean"), _ptr(rstd, "rstd"), _dt(x.dtype), w, _STREAM)
+    return (out, mean, rstd) if mean is not None or rstd is not None else out
+
+
+def ret_layernorm_backward_workspace_bytes(rows: int, d: int) -> int:
+    """Workspace bytes of ret_layernorm_backward's weight gradients."""
+    return int(lib.ret_layernorm_backward_workspace_bytes(int(rows), int(d)))
+
+
+def ret_layernorm_backward(dout, x, mean, rstd, gain=None, dx=None, dgain=None, dbias=None, want_weights: bool = True,
+                           workspace=None, stream=None):
+    """Gradients (dx, dgain, dbias) of ret_layernorm_forward for dout = dL/dout
+    and its mean and rstd; dgain and dbias fp32 [d] (None without
+    ``want_weights``, unless passed in)."""
+    if x.dim() < 1 or x.numel() == 0:
+        raise ValueError("x must be [..., d] with at least one row")
+    d, lead = x.shape[-1], x.shape[:-1]
+    rows = x.numel() // d
+    w = _weight_dt(x, d, gain=gain)
+    dx = torch.empty_like(x) if dx is None else dx
+    if want_weights:
+        dgain = torch.empty(d, dtype=torch.float32, device=x.device) if dgain is None else dgain
+        dbias = torch.empty(d, dtype=torch.float32, device=x.device) if dbias is None else dbias
+    _buf(dout, "dout", x.shape, (x.dtype,), x)
+    _buf(dx, "dx", x.shape, (x.dtype,), x)
+    _buf(mean, "mean", lead, F32, x)
+    _buf(rstd, "rstd", lead, F32, x)
+    _buf(dgain, "dgain", (d,), F32, x)
+    _buf(dbias, "dbias", (d,), F32, x)
+    if workspace is None and (dgain is not None or dbias is not None):
+        workspace = torch.empty(max(ret_layernorm_backward_workspace_bytes(rows, d), 1), dtype=torch.uint8,
+                                device=x.device)
+    _same_device(x, workspace=workspace)
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _call(x, stream, lib.ret_layernorm_backward, _ptr(dout, "dout"), _ptr(x, "x"), _ptr(mean, "mean"),
+          _ptr(rstd, "rstd"), _ptr(gain, "gain"), rows, d, _ptr(dx, "dx"), _ptr(dgain, "dgain"), _ptr(dbias, "dbias"),
+          _dt(x.dtype), w, _ptr(workspace, "workspace"), nbytes, _STREAM)
+    return dx, dgain, dbias
+
+
+def _delta_shapes(q, k, v, g, beta, n_lead: int):
+    """Sizes of a delta-rule call; q, k [*lead, Hk, dk], v [*lead, H, dv], g and beta [*lead, H] fp32."""
+    lead = q.shape[:n_lead]
+    if q.dim() != n_lead + 2 or k.shape != q.shape or v.dim() != n_lead + 2 or v.shape[:n_lead] != lead:
+        raise ValueError("expected q, k [B, N, Hk, dk] and v [B, N, H, dv]" if n_lead == 2 else
+                         "expected q, k [B, Hk, dk] and v [B, H, dv]")
+    if not (q.dtype == k.dtype == v.dtype):
+        raise TypeError("q, k and v must share a dtype")
+    _same_device(q, k=k, v=v)
+    H, dv = v.shape[n_lead:]
+    _buf(g, "g", (*lead, H), F32, q)
+    _buf(beta, "beta", (*lead, H), F32, q)
+    Hk, dk = q.shape[n_lead:]
+    return lead, Hk, H, dk, dv
+
+
+def ret_delta_workspace_bytes(B, N, Hk, H, dk, dv, dtype=torch.bfloat16) -> int:
+    """Workspace bytes of ret_delta_forward_chunkwise (0: none needed)."""
+    return int(lib.ret_delta_workspace_bytes(B, N, Hk, H, dk, dv, _dt(dtype)))
+
+
+def ret_delta_forward_chunkwise(q, k, v, g, beta, lengths=None, initial_state=None, out=None, final_state=None,
+                                out_dtype=None, want_final_state: bool = False, workspace=None, stream=None):
+    """Gated delta rule over a (padded) batch of sequences: q, k [B, N, Hk, dk],
+    v [B, N, H, dv], g (log decay) and beta [B, N, H] fp32, lengths int32 [B] on
+    the device or None, states [B, H, dk, dv] fp32.  Returns ``out`` [B, N, H, dv]
+    (rows behind a sequence's end are not written), or ``(out, final_state)``
+    when a final state is requested (passed in or ``want_final_state``)."""
+    (B, N), Hk, H, dk, dv = _delta_shapes(q, k, v, g, beta, 2)
+    if out is None:
+        out = torch.empty((B, N, H, dv), dtype=out_dtype or q.dtype, device=q.device)
+    if final_state is None and want_final_state:
+        final_state = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+    _seq_outputs(q, out, final_state, B, N, H, dk, dv, initial_state)
+    _buf(lengths, "lengths", (B,), (torch.int32,), q)
+    if workspace is None:
+        nb = ret_delta_workspace_bytes(B, N, Hk, H, dk, dv, q.dtype)
+        workspace = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
+    _same_device(q, workspace=workspace)
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _call(q, stream, lib.ret_delta_forward_chunkwise, _ptr(q, "q"), _ptr(k, "k"), _ptr(v, "v"), _ptr(g, "g"),
+          _ptr(beta, "beta"), _ptr(lengths, "lengths"), _ptr(initial_state, "initial_state"), B, N, Hk, H, dk, dv,
+          _ptr(out, "out"), _ptr(final_state, "final_state"), _STREAM, _dt(q.dtype), _dt(out.dtype),
+          _ptr(workspace, "workspace"), nbytes)
+    return (out, final_state) if final_state is not None else out
+
+
+def ret_delta_decode_step(q, k, v, g, beta, state, out=None, out_dtype=None, stream=None):
+    """One token of the gated delta rule: q, k [B, Hk, dk], v [B, H, dv], g and
+    beta [B, H] fp32, state [B, H, dk, dv] fp32 updated in place; returns out
+    [B, H, dv]."""
+    (B,), Hk, H, dk, dv = _delta_shapes(q, k, v, g, beta, 1)
+    if state is None:
+        raise ValueError("state must be float32 [B, H, dk, dv]")
+    _buf(state, "state", (B, H, dk, dv), F32, q)
+    if out is None:
+        out = torch.empty((B, H, dv), dtype=out_dtype or torch.float32, device=q.device)
+    _buf(out, "out", (B, H, dv), FLOATS, q)
+    _call(q, stream, lib.ret_delta_decode_step, _ptr(q, "q"), _ptr(k, "k"), _ptr(v, "v"), _ptr(g, "g"),
+          _ptr(beta, "beta"), _ptr(state, "state"), _ptr(out, "out"), _STREAM, B, Hk, H, dk, dv, _dt(q.dtype),
+          _dt(out.dtype))
     return out

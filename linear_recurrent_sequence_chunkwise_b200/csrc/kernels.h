@@ -160,4 +160,70 @@ ret_status launch_block(const BlockArgs& a, cudaStream_t s);
 ret_status launch_layernorm(const void* x, const void* gain, const void* bias, void* y, int M, int d, double eps,
                             cudaStream_t s);
 
+// Rotary positions (k_rotary.cu).  A view of [B, N, heads, d] with element
+// strides of batch, token and head; components are consecutive.
+constexpr int kMaxRotaryDim = 512;
+struct RotaryView {
+    void* p;
+    long long sb, sn, sh;
+};
+struct RotaryArgs {
+    RotaryView q, k, qo, ko;      // k, ko unused when Hk is 0
+    const long long* positions;   // device [B, N], or null (pos_offset + n)
+    long long pos_offset;
+    int B, N, H, Hk, d, rotary_dim;
+    int half;                     // pairs (p, p + rotary_dim / 2) instead of (2p, 2p + 1)
+    int inverse;                  // turn by the negative angle (the transpose)
+    float scale;
+    ret_dtype dt;
+};
+// freqs: host, rotary_dim / 2 angles per position.
+ret_status launch_rotary(const RotaryArgs& a, const double* freqs, cudaStream_t s);
+
+// Layer norm and its gradients (k_layernorm.cu), rows of d <= kLayerNormMaxDim.
+constexpr int kLayerNormMaxDim = 8192;
+struct LayerNormArgs {
+    const void *x, *gain, *bias, *dy;  // gain, bias may be null
+    void *y, *dx;
+    float *mean, *rstd;                // written by the forward (may be null), read by the backward
+    float *dgain, *dbias;              // may be null
+    void* workspace;
+    long long rows;
+    int d;
+    double eps;
+    ret_dtype dt, w_dt;                // of x, dy, y, dx; of gain, bias
+};
+size_t layernorm_bwd_workspace_bytes(long long rows, int d);
+ret_status launch_layernorm_forward(const LayerNormArgs& a, cudaStream_t s);
+ret_status launch_layernorm_backward(const LayerNormArgs& a, cudaStream_t s);
+
+// The gated delta rule (k_delta_step.cu, k_delta_chunk.cu, k_delta_backward.cu).
+// Value head h reads key head h / (H / Hk).
+constexpr int kDeltaMaxDk = 256;
+struct DeltaArgs {
+    const void *q, *k, *v;        // [B, N, Hk, dk] twice, [B, N, H, dv]
+    const float *g, *beta;        // [B, N, H]
+    const int* lengths;           // device [B] (clamped to [0, N]), or null
+    const float* initial_state;   // [B, H, dk, dv], or null
+    float* final_state;           // or null
+    void* out;
+    // backward
+    const void* dout;
+    const float* dfinal_state;    // or null
+    void *dq, *dkk, *dvv;         // of dtype grad_dt
+    float *dg, *dbeta, *dinitial_state;  // dinitial_state may be null
+    ret_dtype grad_dt;
+    int B, N, Hk, H, dk, dv;
+    ret_dtype in_dt, out_dt;
+};
+ret_status launch_delta_step(const DeltaArgs& a, float* state, cudaStream_t s);
+// The whole sequence token by token (any dk <= kDeltaMaxDk, any dv).
+ret_status launch_delta_recurrent(const DeltaArgs& a, cudaStream_t s);
+// The chunkwise tensor-core path: bf16, dk 64, 128 or 256, dv a multiple of 8.
+bool delta_chunk_shape_ok(const DeltaArgs& a);
+size_t delta_forward_ws_bytes(const DeltaArgs& a);
+ret_status launch_delta_forward(const DeltaArgs& a, void* ws, cudaStream_t s);
+size_t delta_backward_ws_bytes(const DeltaArgs& a);
+ret_status launch_delta_backward(const DeltaArgs& a, void* ws, cudaStream_t s);
+
 }  // namespace ret

@@ -95,6 +95,82 @@ static ret_status make_args(RetArgs* a, const char* who, const void* q, const vo
     return RET_OK;
 }
 
+
+// A buffer of a call, for the overlap check: every written one must be apart
+// from all others (null ones are skipped).
+struct Buf {
+    const char* name;
+    const void* p;
+    size_t bytes;
+    bool written;
+};
+
+static ret_status check_apart(const char* who, const Buf* bufs, int n) {
+    for (int i = 0; i < n; i++)
+        for (int j = i + 1; j < n; j++)
+            if (bufs[i].p && bufs[j].p && (bufs[i].written || bufs[j].written) &&
+                overlaps(bufs[i].p, bufs[i].bytes, bufs[j].p, bufs[j].bytes))
+                return fail(RET_ERR_INVALID_ARG, "%s: %s overlaps %s", who, bufs[i].name, bufs[j].name);
+    return RET_OK;
+}
+
+static ret_status check_workspace_buf(const char* who, const void* workspace, size_t bytes, size_t need) {
+    if (!workspace || bytes < need)
+        return fail(RET_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed (got %zu)", who, need,
+                    workspace ? bytes : (size_t)0);
+    if (!aligned(workspace, 256)) return fail(RET_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);
+    return RET_OK;
+}
+
+// ---- rotary views
+
+// Elements from the first to one past the last of a view.
+static size_t view_extent(const RotaryView& v, int B, int N, int H, int d) {
+    return (size_t)((B - 1) * v.sb + (N - 1) * v.sn + (H - 1) * v.sh + d);
+}
+
+// No two (batch, token, head) rows of a written view share an element.
+static bool view_rows_apart(const RotaryView& v, int B, int N, int H, int d) {
+    struct Axis {
+        long long stride, count;
+    } ax[3] = {{v.sb, B}, {v.sn, N}, {v.sh, H}};
+    for (int i = 0; i < 3; i++)
+        for (int j = i + 1; j < 3; j++)
+            if (ax[j].stride < ax[i].stride) {
+                const Axis t = ax[i];
+                ax[i] = ax[j];
+                ax[j] = t;
+            }
+    long long reach = d;
+    for (const Axis& x : ax) {
+        if (x.count == 1) continue;
+        if (x.stride < reach) return false;
+        reach = x.stride * (x.count - 1) + reach;
+    }
+    return true;
+}
+
+// Two views share no element: their extents are apart, or they have the same
+// batch and token strides and their rows lie side by side within a token.
+static bool views_apart(const RotaryView& x, int hx, const RotaryView& y, int hy, int B, int N, int d, size_t es) {
+    const size_t ex = view_extent(x, B, N, hx, d) * es, ey = view_extent(y, B, N, hy, d) * es;
+    if (!overlaps(x.p, ex, y.p, ey)) return true;
+    if ((B > 1 && x.sb != y.sb) || (N > 1 && x.sn != y.sn)) return false;
+    const RotaryView &lo = x.p <= y.p ? x : y, &hi = x.p <= y.p ? y : x;
+    const int hl = x.p <= y.p ? hx : hy, hh = x.p <= y.p ? hy : hx;
+    const long long delta = (long long)((const char*)hi.p - (const char*)lo.p);
+    const long long wl = ((hl - 1) * lo.sh + d) * (long long)es, wh = ((hh - 1) * hi.sh + d) * (long long)es;
+    // the smallest distance between two tokens' rows
+    long long token = N > 1 ? x.sn : B > 1 ? x.sb : 0;
+    if (N > 1 && B > 1) {
+        const bool tokens_inside = x.sn <= x.sb;
+        const long long inner = tokens_inside ? x.sn : x.sb, outer = tokens_inside ? x.sb : x.sn;
+        const long long gap = outer - inner * ((tokens_inside ? N : B) - 1);
+        token = inner < gap ? inner : gap;
+    }
+    return wl <= delta && (token == 0 || delta + wh <= token * (long long)es);
+}
+
 }  // namespace ret
 
 using namespace ret;
@@ -705,6 +781,248 @@ ret_status ret_linear_bf16(const void* X, const void* W, void* Y, int M, int N, 
     return launch_linear(X, W, Y, M, N, K, out_dt, stream);
 }
 
+ret_status ret_rotary_frequencies(int rotary_dim, double theta_base, int scaling, double factor,
+                                  double original_length, double beta_fast, double beta_slow, double* freqs,
+                                  double* scale) {
+    t_err[0] = 0;
+    const char* who = "ret_rotary_frequencies";
+    if (!freqs || !scale) return fail(RET_ERR_INVALID_ARG, "%s: NULL freqs or scale", who);
+    if (rotary_dim < 2 || rotary_dim % 2 || rotary_dim > kMaxRotaryDim)
+        return fail(RET_ERR_INVALID_ARG, "%s: rotary_dim must be even, in [2, %d]", who, kMaxRotaryDim);
+    if (!(theta_base > 0.0 && isfinite(theta_base)))
+        return fail(RET_ERR_INVALID_ARG, "%s: theta_base must be finite and > 0", who);
+    if (scaling != RET_ROTARY_PLAIN && scaling != RET_ROTARY_LINEAR && scaling != RET_ROTARY_YARN)
+        return fail(RET_ERR_INVALID_ARG, "%s: unknown scaling %d", who, scaling);
+    if (scaling != RET_ROTARY_PLAIN && !(factor >= 1.0 && isfinite(factor)))
+        return fail(RET_ERR_INVALID_ARG, "%s: factor must be finite and >= 1", who);
+    double low = 0.0, high = 0.0;
+    if (scaling == RET_ROTARY_YARN) {
+        if (!(theta_base > 1.0)) return fail(RET_ERR_INVALID_ARG, "%s: theta_base must be > 1 for this scaling", who);
+        if (!(original_length > 0.0 && isfinite(original_length) && beta_slow > 0.0 && beta_fast > beta_slow &&
+              isfinite(beta_fast)))
+            return fail(RET_ERR_INVALID_ARG, "%s: original_length > 0 and beta_fast > beta_slow > 0 needed", who);
+        // the pair index that turns `turns` times over original_length tokens
+        const double two_pi = 6.283185307179586476925286766559;
+        auto index = [&](double turns) {
+            return rotary_dim * log(original_length / (turns * two_pi)) / (2.0 * log(theta_base));
+        };
+        low = fmax(floor(index(beta_fast)), 0.0);
+        high = fmin(ceil(index(beta_slow)), (double)(rotary_dim - 1));
+    }
+    for (int p = 0; p < rotary_dim / 2; p++) {
+        const double f = pow(theta_base, -2.0 * p / rotary_dim);
+        double ramp = 0.0;
+        if (scaling == RET_ROTARY_YARN) ramp = fmin(fmax((p - low) / fmax(high - low, 1e-3), 0.0), 1.0);
+        if (scaling == RET_ROTARY_LINEAR) ramp = 1.0;
+        freqs[p] = scaling == RET_ROTARY_PLAIN ? f : f * (1.0 - ramp) + f / factor * ramp;
+    }
+    *scale = scaling == RET_ROTARY_YARN ? 0.1 * log(factor) + 1.0 : 1.0;
+    return RET_OK;
+}
+
+ret_status ret_rotary(const void* q, const void* k, void* q_out, void* k_out, const int64_t* q_strides,
+                      const int64_t* k_strides, const int64_t* q_out_strides, const int64_t* k_out_strides,
+                      const double* freqs, double scale, const int64_t* positions, int64_t pos_offset, int inverse,
+                      int layout, int B, int N, int H, int Hk, int d, int rotary_dim, ret_dtype dt,
+                      cudaStream_t stream) {
+    t_err[0] = 0;
+    const char* who = "ret_rotary";
+    if (!q || !q_out || !freqs) return fail(RET_ERR_INVALID_ARG, "%s: NULL q, q_out or freqs", who);
+    if (!k != !k_out) return fail(RET_ERR_INVALID_ARG, "%s: k and k_out go together", who);
+    if (!is_dtype(dt)) return fail(RET_ERR_INVALID_ARG, "%s: unknown dtype", who);
+    if (B < 1 || N < 1 || H < 1 || (k && Hk < 1) || d < 2 || d % 2)
+        return fail(RET_ERR_INVALID_ARG, "%s: sizes must be >= 1 and d even >= 2", who);
+    if (!k) Hk = 0;
+    if (H > 65535 || Hk > 65535) return fail(RET_ERR_INVALID_ARG, "%s: at most 65535 heads", who);
+    if (rotary_dim < 2 || rotary_dim % 2 || rotary_dim > d || rotary_dim > kMaxRotaryDim)
+        return fail(RET_ERR_INVALID_ARG, "%s: rotary_dim must be even, in [2, min(d, %d)]", who, kMaxRotaryDim);
+    if (layout != RET_ROTARY_INTERLEAVED && layout != RET_ROTARY_HALF)
+        return fail(RET_ERR_INVALID_ARG, "%s: unknown layout %d", who, layout);
+    if (!isfinite(scale)) return fail(RET_ERR_INVALID_ARG, "%s: scale must be finite", who);
+    for (int p = 0; p < rotary_dim / 2; p++)
+        if (!isfinite(freqs[p])) return fail(RET_ERR_INVALID_ARG, "%s: freqs[%d] is not finite", who, p);
+    if ((long long)B * N >= (1ll << 31) - 65536 || (long long)(H + Hk) * d >= (1ll << 31) - 65536)
+        return fail(RET_ERR_INVALID_ARG, "%s: problem too large", who);
+    const size_t es = esize(dt);
+    for (const void* ptr : {q, k, (const void*)q_out, (const void*)k_out})
+        if (ptr && !aligned(ptr, es)) return fail(RET_ERR_INVALID_ARG, "%s: pointers must be aligned to their element", who);
+    if (positions && !aligned(positions, 8)) return fail(RET_ERR_INVALID_ARG, "%s: positions must be 8-byte aligned", who);
+    RotaryArgs a{};
+    auto view = [&](RotaryView* v, const void* p, const int64_t* st, int heads) {
+        v->p = const_cast<void*>(p);
+        v->sh = st ? st[2] : d;
+        v->sn = st ? st[1] : (long long)heads * d;
+        v->sb = st ? st[0] : (long long)N * heads * d;
+        const double reach = (double)(B - 1) * v->sb + (double)(N - 1) * v->sn + (double)(heads - 1) * v->sh;
+        return v->sb >= 0 && v->sn >= 0 && v->sh >= 0 && reach < 1e14;
+    };
+    if (!view(&a.q, q, q_strides, H) || !view(&a.qo, q_out, q_out_strides, H) ||
+        (k && (!view(&a.k, k, k_strides, Hk) || !view(&a.ko, k_out, k_out_strides, Hk))))
+        return fail(RET_ERR_INVALID_ARG, "%s: strides must be >= 0 and a view within 10^14 elements", who);
+    if (!view_rows_apart(a.qo, B, N, H, d) || (k && !view_rows_apart(a.ko, B, N, Hk, d)))
+        return fail(RET_ERR_INVALID_ARG, "%s: rows of an output share elements", who);
+    auto same = [](const RotaryView& x, const RotaryView& y) {
+        return x.p == y.p && x.sb == y.sb && x.sn == y.sn && x.sh == y.sh;
+    };
+    bool ok = same(a.q, a.qo) || views_apart(a.q, H, a.qo, H, B, N, d, es);
+    if (k)
+        ok = ok && (same(a.k, a.ko) || views_apart(a.k, Hk, a.ko, Hk, B, N, d, es)) &&
+             views_apart(a.q, H, a.ko, Hk, B, N, d, es) && views_apart(a.k, Hk, a.qo, H, B, N, d, es) &&
+             views_apart(a.qo, H, a.ko, Hk, B, N, d, es);
+    if (ok && positions) {
+        const size_t np = (size_t)B * N * 8;
+        ok = !overlaps(positions, np, q_out, view_extent(a.qo, B, N, H, d) * es) &&
+             (!k || !overlaps(positions, np, k_out, view_extent(a.ko, B, N, Hk, d) * es));
+    }
+    if (!ok) return fail(RET_ERR_INVALID_ARG, "%s: an output overlaps another buffer", who);
+    a.positions = reinterpret_cast<const long long*>(positions);
+    a.pos_offset = pos_offset;
+    a.B = B; a.N = N; a.H = H; a.Hk = Hk; a.d = d; a.rotary_dim = rotary_dim;
+    a.half = layout == RET_ROTARY_HALF;
+    a.inverse = inverse ? 1 : 0;
+    a.scale = (float)scale;
+    a.dt = dt;
+    return launch_rotary(a, freqs, stream);
+}
+
+static ret_status check_layernorm(const char* who, const LayerNormArgs& a) {
+    if (a.rows < 1 || a.d < 1) return fail(RET_ERR_INVALID_ARG, "%s: sizes must be >= 1", who);
+    if (!is_dtype(a.dt) || !is_dtype(a.w_dt)) return fail(RET_ERR_INVALID_ARG, "%s: unknown dtype", who);
+    if (a.rows >= (1ll << 31)) return fail(RET_ERR_INVALID_ARG, "%s: fewer than 2^31 rows", who);
+    if (a.d > kLayerNormMaxDim) return fail(RET_ERR_UNSUPPORTED, "%s: d above %d", who, kLayerNormMaxDim);
+    for (const void* p : {a.x, a.dy, (const void*)a.y, (const void*)a.dx})
+        if (!aligned(p, esize(a.dt))) return fail(RET_ERR_INVALID_ARG, "%s: pointers must be aligned to their element", who);
+    for (const void* p : {a.gain, a.bias})
+        if (!aligned(p, esize(a.w_dt))) return fail(RET_ERR_INVALID_ARG, "%s: pointers must be aligned to their element", who);
+    for (const float* p : {a.mean, a.rstd, a.dgain, a.dbias})
+        if (!aligned(p, 4)) return fail(RET_ERR_INVALID_ARG, "%s: pointers must be aligned to their element", who);
+    return RET_OK;
+}
+
+ret_status ret_layernorm_forward(const void* x, const void* gain, const void* bias, double eps, int64_t rows, int d,
+                                 void* y, float* mean, float* rstd, ret_dtype dt, ret_dtype w_dt,
+                                 cudaStream_t stream) {
+    t_err[0] = 0;
+    const char* who = "ret_layernorm_forward";
+    if (!x || !y) return fail(RET_ERR_INVALID_ARG, "%s: NULL x or y", who);
+    if (!(eps >= 0.0 && isfinite(eps))) return fail(RET_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", who);
+    LayerNormArgs a{};
+    a.x = x; a.gain = gain; a.bias = bias; a.y = y; a.mean = mean; a.rstd = rstd;
+    a.rows = rows; a.d = d; a.eps = eps; a.dt = dt; a.w_dt = w_dt;
+    ret_status st = check_layernorm(who, a);
+    if (st != RET_OK) return st;
+    const size_t n = (size_t)rows * d * esize(dt), nw = (size_t)d * esize(w_dt), ns = (size_t)rows * 4;
+    const Buf bufs[] = {{"x", x, n, false}, {"gain", gain, nw, false}, {"bias", bias, nw, false},
+                        {"y", y, n, true}, {"mean", mean, ns, true}, {"rstd", rstd, ns, true}};
+    if ((st = check_apart(who, bufs, 6)) != RET_OK) return st;
+    return launch_layernorm_forward(a, stream);
+}
+
+size_t ret_layernorm_backward_workspace_bytes(int64_t rows, int d) {
+    if (rows < 1 || d < 1 || d > kLayerNormMaxDim) return 0;
+    return layernorm_bwd_workspace_bytes(rows, d);
+}
+
+ret_status ret_layernorm_backward(const void* dy, const void* x, const float* mean, const float* rstd,
+                                  const void* gain, int64_t rows, int d, void* dx, float* dgain, float* dbias,
+                                  ret_dtype dt, ret_dtype w_dt, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream) {
+    t_err[0] = 0;
+    const char* who = "ret_layernorm_backward";
+    if (!dy || !x || !mean || !rstd) return fail(RET_ERR_INVALID_ARG, "%s: NULL dy, x, mean or rstd", who);
+    if (!dx && !dgain && !dbias) return fail(RET_ERR_INVALID_ARG, "%s: no gradient wanted", who);
+    LayerNormArgs a{};
+    a.x = x; a.dy = dy; a.gain = gain; a.dx = dx; a.dgain = dgain; a.dbias = dbias;
+    a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
+    a.rows = rows; a.d = d; a.dt = dt; a.w_dt = w_dt;
+    ret_status st = check_layernorm(who, a);
+    if (st != RET_OK) return st;
+    const size_t need = dgain || dbias ? layernorm_bwd_workspace_bytes(rows, d) : 0;
+    if (need && (st = check_workspace_buf(who, workspace, workspace_bytes, need)) != RET_OK) return st;
+    a.workspace = need ? workspace : nullptr;
+    const size_t n = (size_t)rows * d * esize(dt), nw = (size_t)d * esize(w_dt), ns = (size_t)rows * 4;
+    const Buf bufs[] = {{"dy", dy, n, false}, {"x", x, n, false}, {"mean", mean, ns, false}, {"rstd", rstd, ns, false},
+                        {"gain", gain, nw, false}, {"dx", dx, n, true}, {"dgain", dgain, (size_t)d * 4, true},
+                        {"dbias", dbias, (size_t)d * 4, true}, {"workspace", a.workspace, need, true}};
+    if ((st = check_apart(who, bufs, 9)) != RET_OK) return st;
+    return launch_layernorm_backward(a, stream);
+}
+
+// Sizes, dtypes and alignment shared by the delta rule's entry points.
+static ret_status check_delta(const char* who, const DeltaArgs& a) {
+    if (!a.q || !a.k || !a.v || !a.g || !a.beta) return fail(RET_ERR_INVALID_ARG, "%s: NULL q, k, v, g or beta", who);
+    if (a.B < 1 || a.N < 1 || a.Hk < 1 || a.H < 1 || a.dk < 1 || a.dv < 1)
+        return fail(RET_ERR_INVALID_ARG, "%s: sizes must be >= 1 (B=%d N=%d Hk=%d H=%d dk=%d dv=%d)", who, a.B, a.N, a.Hk,
+                    a.H, a.dk, a.dv);
+    if (a.H % a.Hk) return fail(RET_ERR_INVALID_ARG, "%s: H=%d is not a multiple of Hk=%d", who, a.H, a.Hk);
+    if (a.B > 65535 || a.H > 65535) return fail(RET_ERR_INVALID_ARG, "%s: at most 65535 sequences and heads", who);
+    if (!is_dtype(a.in_dt) || !is_dtype(a.out_dt)) return fail(RET_ERR_INVALID_ARG, "%s: unknown dtype", who);
+    if (a.dk > kDeltaMaxDk) return fail(RET_ERR_UNSUPPORTED, "%s: dk above %d", who, kDeltaMaxDk);
+    if ((size_t)a.B * a.N * a.H * (size_t)(a.dk > a.dv ? a.dk : a.dv) > ((size_t)1 << 40) ||
+        (size_t)a.B * a.H * ((a.dv + 15) / 16) >= ((size_t)1 << 31))
+        return fail(RET_ERR_INVALID_ARG, "%s: problem too large", who);
+    for (const void* p : {a.q, a.k, a.v, (const void*)a.initial_state, (const void*)a.final_state, (const void*)a.out})
+        if (!aligned(p, 16))
+            return fail(RET_ERR_INVALID_ARG, "%s: q, k, v, out and the states must be 16-byte aligned", who);
+    for (const void* p : {(const void*)a.g, (const void*)a.beta, (const void*)a.lengths})
+        if (!aligned(p, 4)) return fail(RET_ERR_INVALID_ARG, "%s: g, beta and lengths must be 4-byte aligned", who);
+    return RET_OK;
+}
+
+size_t ret_delta_workspace_bytes(int B, int N, int Hk, int H, int dk, int dv, ret_dtype in_dt) {
+    if (B < 1 || N < 1 || Hk < 1 || H < 1 || dk < 1 || dv < 1 || H % Hk) return 0;
+    DeltaArgs a{};
+    a.B = B; a.N = N; a.Hk = Hk; a.H = H; a.dk = dk; a.dv = dv; a.in_dt = in_dt;
+    return delta_chunk_shape_ok(a) ? delta_forward_ws_bytes(a) : 0;
+}
+
+ret_status ret_delta_forward_chunkwise(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                                       const int32_t* lengths, const float* initial_state, int B, int N, int Hk,
+                                       int H, int dk, int dv, void* out, float* final_state, cudaStream_t stream,
+                                       ret_dtype in_dt, ret_dtype out_dt, void* workspace, size_t workspace_bytes) {
+    t_err[0] = 0;
+    const char* who = "ret_delta_forward_chunkwise";
+    DeltaArgs a{};
+    a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.lengths = lengths;
+    a.initial_state = initial_state; a.final_state = final_state; a.out = out;
+    a.B = B; a.N = N; a.Hk = Hk; a.H = H; a.dk = dk; a.dv = dv; a.in_dt = in_dt; a.out_dt = out_dt;
+    ret_status st = check_delta(who, a);
+    if (st != RET_OK) return st;
+    if (!out) return fail(RET_ERR_INVALID_ARG, "%s: out is NULL", who);
+    const bool chunked = delta_chunk_shape_ok(a);
+    const size_t need = chunked ? delta_forward_ws_bytes(a) : 0;
+    if (chunked && (st = check_workspace_buf(who, workspace, workspace_bytes, need)) != RET_OK) return st;
+    const size_t tok = (size_t)B * N, nq = tok * Hk * dk * esize(in_dt), nv = tok * H * dv, ng = tok * H * 4;
+    const size_t ns = (size_t)B * H * dk * dv * 4;
+    const Buf bufs[] = {{"q", q, nq, false}, {"k", k, nq, false}, {"v", v, nv * esize(in_dt), false},
+                        {"g", g, ng, false}, {"beta", beta, ng, false}, {"lengths", lengths, (size_t)B * 4, false},
+                        {"initial_state", initial_state == final_state ? nullptr : initial_state, ns, false},
+                        {"out", out, nv * esize(out_dt), true}, {"final_state", final_state, ns, true},
+                        {"workspace", chunked ? workspace : nullptr, need, true}};
+    if ((st = check_apart(who, bufs, 10)) != RET_OK) return st;
+    return chunked ? launch_delta_forward(a, workspace, stream) : launch_delta_recurrent(a, stream);
+}
+
+ret_status ret_delta_decode_step(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                                 float* state, void* out, cudaStream_t stream, int B, int Hk, int H, int dk, int dv,
+                                 ret_dtype in_dt, ret_dtype out_dt) {
+    t_err[0] = 0;
+    const char* who = "ret_delta_decode_step";
+    DeltaArgs a{};
+    a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.final_state = state; a.out = out;
+    a.B = B; a.N = 1; a.Hk = Hk; a.H = H; a.dk = dk; a.dv = dv; a.in_dt = in_dt; a.out_dt = out_dt;
+    ret_status st = check_delta(who, a);
+    if (st != RET_OK) return st;
+    if (!state || !out) return fail(RET_ERR_INVALID_ARG, "%s: NULL state or out", who);
+    if (dv % 4) return fail(RET_ERR_INVALID_ARG, "%s: dv must be a multiple of 4 (got %d)", who, dv);
+    const size_t nq = (size_t)B * Hk * dk * esize(in_dt), nv = (size_t)B * H * dv, ng = (size_t)B * H * 4;
+    const Buf bufs[] = {{"q", q, nq, false}, {"k", k, nq, false}, {"v", v, nv * esize(in_dt), false},
+                        {"g", g, ng, false}, {"beta", beta, ng, false}, {"state", state, nv * dk * 4, true},
+                        {"out", out, nv * esize(out_dt), true}};
+    if ((st = check_apart(who, bufs, 7)) != RET_OK) return st;
+    return launch_delta_step(a, state, stream);
+}
+
 ret_status ret_selftest_bounded_wait(uint32_t polls, cudaStream_t stream) {
     t_err[0] = 0;
     if (polls < 1 || polls > (1u << 24))
@@ -716,11 +1034,12 @@ ret_status ret_check_device_error(cudaStream_t stream) {
     t_err[0] = 0;
     cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return fail(RET_ERR_CUDA, "ret_check_device_error: %s", cudaGetErrorString(e));
-    int flag = 0, flag2 = 0;
+    int flag = 0, flag2 = 0, flag3 = 0;
     e = read_clear_error_chunk_ws(&flag);
     if (e == cudaSuccess) e = read_clear_error_gemm(&flag2);
+    if (e == cudaSuccess) e = read_clear_error_delta(&flag3);
     if (e != cudaSuccess) return fail(RET_ERR_CUDA, "ret_check_device_error: %s", cudaGetErrorString(e));
-    flag |= flag2;
+    flag |= flag2 | flag3;
     if (flag) return fail(RET_ERR_TIMEOUT, "a kernel gave up a bounded wait (device error word %d)", flag);
     return RET_OK;
 }
