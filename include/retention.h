@@ -571,6 +571,19 @@ ret_status ret_layernorm_backward(const void* dy, const void* x, const float* me
  *
  * ret_delta_decode_step: one token; q, k [B, Hk, dk], v, out [B, H, dv],
  *   g, beta [B, H], state updated in place, dv a multiple of 4.
+ *
+ * ret_delta_backward_chunkwise: gradients of a loss L for dout = dL/dout [B, N,
+ *   H, dv] (bf16) and dfinal_state = dL/dfinal_state (fp32, or NULL: zero), of
+ *   the forward with the same q, k, v, g, beta, lengths and initial_state:
+ *   dq, dk [B, N, Hk, dk] and dv [B, N, H, dv] of dtype grad_dt, dg and dbeta
+ *   [B, N, H] fp32, dinitial_state fp32 (or NULL: not wanted; without an
+ *   initial_state it is the gradient at zero).  A key head's gradient is the sum
+ *   over its value heads, in a fixed order: a call on the same inputs gives the
+ *   same bits.  Rows behind a sequence's end get zeros.  The states are computed
+ *   again and kept in the workspace (device, 256-byte aligned, overlapping
+ *   nothing) of ret_delta_backward_workspace_bytes(...) bytes.  bf16 inputs with
+ *   dk 64, 128 or 256 and dv a multiple of 8, else RET_ERR_UNSUPPORTED (the size
+ *   is 0 then).  All pointers aligned as for the forward, gradients 16-byte.
  */
 size_t ret_delta_workspace_bytes(int B, int N, int Hk, int H, int dk, int dv, ret_dtype in_dt);
 
@@ -583,6 +596,15 @@ ret_status ret_delta_forward_chunkwise(const void* q, const void* k, const void*
 ret_status ret_delta_decode_step(const void* q, const void* k, const void* v, const float* g, const float* beta,
                                  float* state, void* out, cudaStream_t stream, int B, int Hk, int H, int dk, int dv,
                                  ret_dtype in_dt, ret_dtype out_dt);
+
+size_t ret_delta_backward_workspace_bytes(int B, int N, int Hk, int H, int dk, int dv, ret_dtype in_dt);
+
+ret_status ret_delta_backward_chunkwise(const void* q, const void* k, const void* v, const float* g,
+                                        const float* beta, const void* dout, const int32_t* lengths,
+                                        const float* initial_state, const float* dfinal_state, int B, int N, int Hk,
+                                        int H, int dk, int dv, void* dq, void* dk_out, void* dv_out, float* dg,
+                                        float* dbeta, float* dinitial_state, cudaStream_t stream, ret_dtype in_dt,
+                                        ret_dtype grad_dt, void* workspace, size_t workspace_bytes);
 
 /*
  * Diagnostics: one device thread waits on a barrier that nothing arrives on,

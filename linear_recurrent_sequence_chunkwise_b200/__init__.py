@@ -31,6 +31,7 @@ __all__ = [
     "ret_rotary", "ret_rotary_frequencies", "ret_layernorm_forward", "ret_layernorm_backward",
     "ret_layernorm_backward_workspace_bytes",
     "ret_delta_forward_chunkwise", "ret_delta_workspace_bytes", "ret_delta_decode_step",
+    "ret_delta_backward_chunkwise", "ret_delta_backward_workspace_bytes",
     "RET_OK", "RET_ERR_INVALID_ARG", "RET_ERR_UNSUPPORTED", "RET_ERR_CUDA", "RET_ERR_TIMEOUT",
     "RET_F32", "RET_BF16",
 ]
@@ -104,6 +105,9 @@ def _load_library():
     L.ret_delta_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
     L.ret_delta_workspace_bytes.restype = ctypes.c_size_t
     L.ret_delta_forward_chunkwise.argtypes = [vp] * 7 + [i] * 6 + [vp, vp, vp, i, i, vp, ctypes.c_size_t]
+    L.ret_delta_backward_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+    L.ret_delta_backward_workspace_bytes.restype = ctypes.c_size_t
+    L.ret_delta_backward_chunkwise.argtypes = [vp] * 9 + [i] * 6 + [vp] * 7 + [i, i, vp, ctypes.c_size_t]
     L.ret_delta_decode_step.argtypes = [vp] * 8 + [i] * 7
     L.ret_check_device_error.argtypes = [vp]
     L.ret_last_error_string.restype = ctypes.c_char_p
@@ -818,3 +822,47 @@ def ret_delta_decode_step(q, k, v, g, beta, state, out=None, out_dtype=None, str
           _ptr(beta, "beta"), _ptr(state, "state"), _ptr(out, "out"), _STREAM, B, Hk, H, dk, dv, _dt(q.dtype),
           _dt(out.dtype))
     return out
+
+
+def ret_delta_backward_workspace_bytes(B, N, Hk, H, dk, dv, dtype=torch.bfloat16) -> int:
+    """Workspace bytes of ret_delta_backward_chunkwise (0: shape not supported)."""
+    return int(lib.ret_delta_backward_workspace_bytes(B, N, Hk, H, dk, dv, _dt(dtype)))
+
+
+def ret_delta_backward_chunkwise(q, k, v, g, beta, dout, lengths=None, initial_state=None, dfinal_state=None, dq=None,
+                                 dk=None, dv=None, dg=None, dbeta=None, dinitial_state=None, grad_dtype=torch.float32,
+                                 want_dinitial_state: Optional[bool] = None, workspace=None, stream=None):
+    """Gradients of ret_delta_forward_chunkwise for dout = dL/dout and
+    dfinal_state = dL/dfinal_state (or None): (dq, dk, dv, dg, dbeta,
+    dinitial_state); dq, dk, dv of ``grad_dtype``, the others fp32.
+    dinitial_state is None unless an initial state is given, it is passed in
+    or wanted."""
+    (B, N), Hk, H, dk_, dv_ = _delta_shapes(q, k, v, g, beta, 2)
+    _buf(dout, "dout", (B, N, H, dv_), (q.dtype,), q)
+    _buf(initial_state, "initial_state", (B, H, dk_, dv_), F32, q)
+    _buf(dfinal_state, "dfinal_state", (B, H, dk_, dv_), F32, q)
+    _buf(lengths, "lengths", (B,), (torch.int32,), q)
+    dq = torch.empty((B, N, Hk, dk_), dtype=grad_dtype, device=q.device) if dq is None else dq
+    dk = torch.empty((B, N, Hk, dk_), dtype=dq.dtype, device=q.device) if dk is None else dk
+    dv = torch.empty((B, N, H, dv_), dtype=dq.dtype, device=q.device) if dv is None else dv
+    dg = torch.empty((B, N, H), dtype=torch.float32, device=q.device) if dg is None else dg
+    dbeta = torch.empty((B, N, H), dtype=torch.float32, device=q.device) if dbeta is None else dbeta
+    if dinitial_state is None and (initial_state is not None if want_dinitial_state is None else want_dinitial_state):
+        dinitial_state = torch.empty((B, H, dk_, dv_), dtype=torch.float32, device=q.device)
+    _buf(dq, "dq", (B, N, Hk, dk_), FLOATS, q)
+    _buf(dk, "dk", (B, N, Hk, dk_), (dq.dtype,), q)
+    _buf(dv, "dv", (B, N, H, dv_), (dq.dtype,), q)
+    _buf(dg, "dg", (B, N, H), F32, q)
+    _buf(dbeta, "dbeta", (B, N, H), F32, q)
+    _buf(dinitial_state, "dinitial_state", (B, H, dk_, dv_), F32, q)
+    if workspace is None:
+        nb = ret_delta_backward_workspace_bytes(B, N, Hk, H, dk_, dv_, q.dtype)
+        workspace = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
+    _same_device(q, workspace=workspace)
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _call(q, stream, lib.ret_delta_backward_chunkwise, _ptr(q, "q"), _ptr(k, "k"), _ptr(v, "v"), _ptr(g, "g"),
+          _ptr(beta, "beta"), _ptr(dout, "dout"), _ptr(lengths, "lengths"), _ptr(initial_state, "initial_state"),
+          _ptr(dfinal_state, "dfinal_state"), B, N, Hk, H, dk_, dv_, _ptr(dq, "dq"), _ptr(dk, "dk"), _ptr(dv, "dv"),
+          _ptr(dg, "dg"), _ptr(dbeta, "dbeta"), _ptr(dinitial_state, "dinitial_state"), _STREAM, _dt(q.dtype),
+          _dt(dq.dtype), _ptr(workspace, "workspace"), nbytes)
+    return dq, dk, dv, dg, dbeta, dinitial_state

@@ -44,6 +44,7 @@ inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_
 constexpr int kErrTimeout = 1;
 cudaError_t read_clear_error_chunk_ws(int* flag);
 cudaError_t read_clear_error_delta(int* flag);
+cudaError_t read_clear_error_delta_grads(int* flag);
 
 // ---------------------------------------------------------------- device side
 

@@ -21,6 +21,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_util.cuh"
+#include "tmap.h"
 
 namespace ret {
 namespace delta {
@@ -28,18 +29,13 @@ namespace delta {
 constexpr int C = 64;              // tokens of a chunk
 constexpr int kTile = C * C * 2;   // bytes of a 64 x 64 bf16 tile (128-byte rows, swizzled)
 constexpr int kSlice = 64;         // value columns of a tile
-constexpr int kGates = 4 * C;      // floats: exp(G), exp(G_C - G), beta, G
+constexpr int kGates = 3 * C * 4;       // bytes: exp(G), exp(G_C - G), beta in fp32
+constexpr int kGateRow = kGates + C * 8;  // and G in 64 bits
 // Below this a decay is zero in fp32; keeps -inf out of the sums.
 constexpr float kMinG = -128.f;
 
-// Workspace of the forward, per (b, h, chunk): T hi, T lo, P hi, P lo; gates.
-struct Layout {
-    int nc, H;
-    __host__ __device__ size_t chunk(int b, int h, int c) const { return ((size_t)b * H + h) * nc + c; }
-};
-
-__host__ inline int chunks_of(int N) { return (N + C - 1) / C; }
-__host__ inline int slices_of(int dv) { return (dv + kSlice - 1) / kSlice; }
+inline int chunks_of(int N) { return (N + C - 1) / C; }
+inline int slices_of(int dv) { return (dv + kSlice - 1) / kSlice; }
 
 __device__ __forceinline__ int length_of(const int* lengths, int b, int N) {
     return lengths ? max(0, min(lengths[b], N)) : N;
@@ -120,8 +116,34 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
+// Clears rows L .. 63 of a tile of `pieces` 16-byte pieces a row (a warp's work).
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int L, int pieces, int lane) {
+    for (int i = lane; i < (C - L) * pieces; i += 32)
+        *reinterpret_cast<uint4*>(tile + tile_at(0, L + i / pieces, i % pieces)) = make_uint4(0, 0, 0, 0);
+}
+
+// [B, N, heads, d] bf16 as a {d, heads, N, B} tensor, boxes of one head's
+// chunk, 64 columns wide.
+inline bool chunk_map(CUtensorMap* m, const void* p, int B, int N, int heads, int d) {
+    const uint64_t dims[4] = {(uint64_t)d, (uint64_t)heads, (uint64_t)N, (uint64_t)B};
+    const uint64_t strides[3] = {(uint64_t)d * 2, (uint64_t)heads * d * 2, (uint64_t)N * heads * d * 2};
+    const uint32_t box[4] = {64, 1, (uint32_t)C, 1};
+    return make_tmap_bf16(m, p, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 // The chunk tables (k_delta_chunk.cu): T, P and the gates of every chunk.
-ret_status launch_prep(const DeltaArgs& a, uint8_t* tiles, float* gates, cudaStream_t s);
+ret_status launch_prep(const DeltaArgs& a, uint8_t* tiles, uint8_t* gates, cudaStream_t s);
+
+// The backward's two chains (k_delta_chunk.cu).  Per (chunk, slice of 64 value
+// columns), transposed (a row per value column), hi then lo:
+//   s   [dk/64][64][128 B]  the state before the chunk
+//   u   [64][128 B]         the corrections
+//   ds  [dk/64][64][128 B]  the gradient of the state after the chunk
+//   y   [64][128 B]         dY = T^T dU
+struct Kept {
+    uint8_t *s, *u, *ds, *y;
+};
+ret_status launch_chains(const DeltaArgs& a, const uint8_t* tiles, const uint8_t* gates, const Kept& kept, cudaStream_t s);
 
 }  // namespace delta
 }  // namespace ret

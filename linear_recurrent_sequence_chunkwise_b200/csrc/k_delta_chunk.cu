@@ -16,11 +16,10 @@
 #include <algorithm>
 
 #include "delta_util.cuh"
-#include "tmap.h"
 
 namespace ret {
 
-__device__ int g_delta_err = 0;
+static __device__ int g_delta_err = 0;
 
 cudaError_t read_clear_error_delta(int* flag) {
     cudaError_t e = cudaMemcpyFromSymbol(flag, g_delta_err, sizeof(int));
@@ -46,7 +45,7 @@ constexpr int prep_smem() {
 
 template <int DK>
 __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(DeltaArgs a, uint8_t* __restrict__ tiles,
-                                                            float* __restrict__ gates, int nc) {
+                                                            uint8_t* __restrict__ gates, int nc) {
     extern __shared__ __align__(1024) uint8_t sm[];
     __shared__ double sG[C];
     __shared__ float sb[C];
@@ -96,11 +95,11 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(DeltaArgs a, uint8_
     }
     __syncthreads();
     if (tid < C) {
-        float* gt = gates + ch * kGates;
+        float* gt = reinterpret_cast<float*>(gates + ch * kGateRow);
         gt[tid] = expf((float)sG[tid]);
         gt[C + tid] = expf((float)(sG[C - 1] - sG[tid]));
         gt[2 * C + tid] = sb[tid];
-        gt[3 * C + tid] = (float)sG[tid];
+        reinterpret_cast<double*>(gt + 3 * C)[tid] = sG[tid];
     }
 
     // a warp takes 16 rows of both score matrices, columns up to the diagonal
@@ -200,7 +199,7 @@ struct Stage {
     static constexpr int G = 1024;
     static constexpr int oQ = K, oT = K + Q, oP = oT + T, oV = oP + P, oG = oV + V;
     static constexpr int bytes = oG + G;
-    static constexpr int loaded = K + Q + T + P + V + kGates * 4;
+    static constexpr int loaded = K + Q + T + P + V + kGates;
     static constexpr int most = 225 * 1024;
     static constexpr int stages = most / bytes > 4 ? 4 : most / bytes;
     static constexpr int smem = stages * bytes + 1024 + 128;
@@ -208,38 +207,48 @@ struct Stage {
 
 struct ChainArgs {
     const uint8_t* tiles;
-    const float* gates;
+    const uint8_t* gates;
     const int* lengths;
     const float* initial_state;
     float* final_state;
     void* out;
-    uint8_t* keep_s;  // kKeep: [chunk][slice][hi, lo][DK/64][64][128 B], the transposed state
-    uint8_t* keep_u;  // kKeep: [chunk][slice][hi, lo][64][128 B], the transposed corrections
+    Kept kept;
     int N, nc, Hk, H, dv;
 };
 
+// The ring's barriers, behind its stages.
+struct Ring {
+    uint8_t* sm;
+    uint64_t *full, *empty;
+    __device__ __forceinline__ void init(int stages, int bytes) {
+        extern __shared__ uint8_t raw[];
+        sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+        full = reinterpret_cast<uint64_t*>(sm + stages * bytes);
+        empty = full + stages;
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < stages; i++) {
+                tc::mbar_init(full + i, 1);
+                tc::mbar_init(empty + i, kWarps);
+            }
+            tc::fence_barrier_init();
+        }
+        __syncthreads();
+    }
+};
+
 template <int DK, int MODE>
-__global__ void __launch_bounds__(kChainThreads, 1)
-    k_delta_chain(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                  const __grid_constant__ CUtensorMap mv, ChainArgs a) {
+__device__ __forceinline__ void chain_forward(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                                              const ChainArgs& a, int b) {
     using St = Stage<DK, MODE>;
     constexpr int NS = St::stages;
-    extern __shared__ uint8_t raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm + NS * St::bytes);
-    uint64_t* empty = full + NS;
-    const int slice = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    Ring ring;
+    ring.init(NS, St::bytes);
+    uint8_t* sm = ring.sm;
+    uint64_t *full = ring.full, *empty = ring.empty;
+    const int slice = blockIdx.x, h = blockIdx.y;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int len = length_of(a.lengths, b, a.N);
     const int n_chunks = (len + C - 1) / C;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < NS; i++) {
-            tc::mbar_init(full + i, 1);
-            tc::mbar_init(empty + i, kWarps);
-        }
-        tc::fence_barrier_init();
-    }
-    __syncthreads();
     const size_t ch0 = ((size_t)b * a.H + h) * a.nc;
 
     if (w == kWarps) {  // loads
@@ -258,7 +267,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             const uint8_t* tl = a.tiles + (ch0 + c) * 4 * kTile;
             bulk_load(s + St::oT, tl, St::T, full + st);
             tc::tma_load_4d(s + St::oV, &mv, full + st, slice * kSlice, h, c * C, b);
-            bulk_load(s + St::oG, a.gates + (ch0 + c) * kGates, kGates * 4, full + st);
+            bulk_load(s + St::oG, a.gates + (ch0 + c) * kGateRow, kGates, full + st);
             if constexpr (MODE != kKeep) {
 #pragma unroll
                 for (int i = 0; i < DK / 64; i++)
@@ -294,10 +303,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         if (L < C) {
             // rows behind the end may hold anything: every warp clears K's for
             // itself (all write the same zeros), V's are never selected
-            for (int i = lane; i < (C - L) * (DK / 8); i += 32) {
-                const int r = L + i / (DK / 8), p = i % (DK / 8);
-                *reinterpret_cast<uint4*>(s + tile_at(0, r, p)) = make_uint4(0, 0, 0, 0);
-            }
+            clear_rows(s, L, DK / 8, lane);
             __syncwarp();
         }
 
@@ -312,7 +318,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             uint32_t hi[4], lo[4];
             split_a(S[2 * kk], S[2 * kk + 1], hi, lo);
             if constexpr (MODE == kKeep) {
-                uint8_t* ks = a.keep_s + ((ch0 + c) * gridDim.x + slice) * (size_t)(4 * C * DK);
+                uint8_t* ks = a.kept.s + ((ch0 + c) * gridDim.x + slice) * (size_t)(4 * C * DK);
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     const uint32_t off = tile_at(0, 16 * w + g + 8 * (e & 1), 2 * kk + (e >> 1)) + 4 * t;
@@ -376,7 +382,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
             }
 
         if constexpr (MODE == kKeep) {
-            uint8_t* ku = a.keep_u + ((ch0 + c) * gridDim.x + slice) * (size_t)(2 * kTile);
+            uint8_t* ku = a.kept.u + ((ch0 + c) * gridDim.x + slice) * (size_t)(2 * kTile);
 #pragma unroll
             for (int n = 0; n < 8; n++)
 #pragma unroll
@@ -538,17 +544,266 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     }
 }
 
-// [B, N, heads, d] bf16 as a {d, heads, N, B} tensor, boxes of one head's
-// chunk, 64 columns wide.
-bool chunk_map(CUtensorMap* m, const void* p, int B, int N, int heads, int d) {
-    const uint64_t dims[4] = {(uint64_t)d, (uint64_t)heads, (uint64_t)N, (uint64_t)B};
-    const uint64_t strides[3] = {(uint64_t)d * 2, (uint64_t)heads * d * 2, (uint64_t)N * heads * d * 2};
-    const uint32_t box[4] = {64, 1, (uint32_t)C, 1};
-    return make_tmap_bf16(m, p, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+// ------------------------------------------------------- the backward's chain
+//
+// With dS1 the gradient of the state after a chunk, and the same T, P:
+//     dU = P^T dO + diag(exp(G_C - G)) K dS1,  dY = T^T dU,  dR = beta dY (= dV)
+//     dS0 = exp(G_C) dS1 + (diag(exp(G)) Q)^T dO - (diag(exp(G)) K)^T dR,
+// column by column as the forward, the chunks from the last to the first.
+
+template <int DK>
+struct BackStage {
+    static constexpr int K = C * DK * 2, Q = K, T = 2 * kTile, P = 2 * kTile, O = C * kSlice * 2, G = 1024;
+    static constexpr int oQ = K, oT = K + Q, oP = oT + T, oO = oP + P, oG = oO + O;
+    static constexpr int bytes = oG + G;
+    static constexpr int loaded = K + Q + T + P + O + kGates;
+    static constexpr int stages = Stage<DK, kKeep>::most / bytes > 3 ? 3 : Stage<DK, kKeep>::most / bytes;
+    static constexpr int smem = stages * bytes + 1024 + 128;
+};
+
+template <int DK>
+__device__ __forceinline__ void chain_backward(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mo,
+                                               const ChainArgs& a, const float* dfinal, float* dinitial, int b) {
+    using St = BackStage<DK>;
+    constexpr int NS = St::stages;
+    Ring ring;
+    ring.init(NS, St::bytes);
+    uint8_t* sm = ring.sm;
+    uint64_t *full = ring.full, *empty = ring.empty;
+    const int slice = blockIdx.x, h = blockIdx.y;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int len = length_of(a.lengths, b, a.N);
+    const int n_chunks = (len + C - 1) / C;
+    const size_t ch0 = ((size_t)b * a.H + h) * a.nc;
+
+    if (w == kWarps) {  // loads
+        if (lane != 0) return;
+        const int hk = h / (a.H / a.Hk);
+        for (int it = 0; it < n_chunks; it++) {
+            const int st = it % NS, c = n_chunks - 1 - it;
+            uint8_t* s = sm + st * St::bytes;
+            if (it >= NS && !tc::mbar_wait(empty + st, ((it / NS) - 1) & 1)) {
+                atomicExch(&g_delta_err, kErrTimeout);
+                return;
+            }
+            tc::mbar_arrive_expect_tx(full + st, St::loaded);
+#pragma unroll
+            for (int i = 0; i < DK / 64; i++) {
+                tc::tma_load_4d(s + i * 8192, &mk, full + st, 64 * i, hk, c * C, b);
+                tc::tma_load_4d(s + St::oQ + i * 8192, &mq, full + st, 64 * i, hk, c * C, b);
+            }
+            bulk_load(s + St::oT, a.tiles + (ch0 + c) * 4 * kTile, St::T + St::P, full + st);
+            tc::tma_load_4d(s + St::oO, &mo, full + st, slice * kSlice, h, c * C, b);
+            bulk_load(s + St::oG, a.gates + (ch0 + c) * kGateRow, kGates, full + st);
+        }
+        return;
+    }
+
+    const int g = lane >> 2, t = lane & 3;
+    const int col = slice * kSlice + 16 * w + g;
+    const size_t sb = ((size_t)b * a.H + h) * DK * a.dv;
+    float S[DK / 8][4];
+#pragma unroll
+    for (int n = 0; n < DK / 8; n++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const int r = 8 * n + 2 * t + (e & 1), cc = col + 8 * (e >> 1);
+            S[n][e] = dfinal && cc < a.dv ? dfinal[sb + (size_t)r * a.dv + cc] : 0.f;
+        }
+
+    for (int it = 0; it < n_chunks; it++) {
+        const int st = it % NS, c = n_chunks - 1 - it;
+        if (!tc::mbar_wait(full + st, (it / NS) & 1)) {
+            if (lane == 0) atomicExch(&g_delta_err, kErrTimeout);
+            return;
+        }
+        uint8_t* s = sm + st * St::bytes;
+        const uint32_t sK = tc::smem_u32(s), sQ = sK + St::oQ, sT = sK + St::oT, sP = sK + St::oP, sO = sK + St::oO;
+        const float* gt = reinterpret_cast<const float*>(s + St::oG);
+        const int L = min(C, len - c * C);
+        if (L < C) {
+            // the last chunk, the first one here: every warp clears what lies
+            // behind the end for itself (all write the same zeros)
+            clear_rows(s, L, DK / 8, lane);
+            clear_rows(s + St::oQ, L, DK / 8, lane);
+            clear_rows(s + St::oO, L, kSlice / 8, lane);
+            __syncwarp();
+        }
+
+        // dU^T = (dS^T K^T) exp(G_C - G) + dO^T P
+        float U[8][4];
+#pragma unroll
+        for (int n = 0; n < 8; n++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) U[n][e] = 0.f;
+        uint8_t* ks = a.kept.ds + ((ch0 + c) * gridDim.x + slice) * (size_t)(4 * C * DK);
+#pragma unroll
+        for (int kk = 0; kk < DK / 16; kk++) {
+            uint32_t hi[4], lo[4];
+            split_a(S[2 * kk], S[2 * kk + 1], hi, lo);
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const uint32_t off = tile_at(0, 16 * w + g + 8 * (e & 1), 2 * kk + (e >> 1)) + 4 * t;
+                *reinterpret_cast<uint32_t*>(ks + off) = hi[e];
+                *reinterpret_cast<uint32_t*>(ks + 2 * C * DK + off) = lo[e];
+            }
+#pragma unroll
+            for (int p = 0; p < 4; p++) {
+                uint32_t bk[4];
+                ldsm4(bk, at_n(sK, 16 * p, 2 * kk, lane));
+                mma(U[2 * p], hi, bk[0], bk[1]);
+                mma(U[2 * p + 1], hi, bk[2], bk[3]);
+                mma(U[2 * p], lo, bk[0], bk[1]);
+                mma(U[2 * p + 1], lo, bk[2], bk[3]);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 8; n++) {
+            const float2 e2 = *reinterpret_cast<const float2*>(gt + C + 8 * n + 2 * t);
+            U[n][0] *= e2.x;
+            U[n][1] *= e2.y;
+            U[n][2] *= e2.x;
+            U[n][3] *= e2.y;
+        }
+        uint32_t oh[4][4], ol[4][4];  // dO^T, later exp(G) dO^T in two terms
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            ldsm4_t(oh[i], at_n(sO, 16 * i, 2 * w, lane));
+#pragma unroll
+            for (int d = 0; d <= i; d++) {  // P is lower triangular: token j takes i >= j
+                uint32_t ph[4], pl[4];
+                ldsm4_t(ph, at_k(sP, 16 * i, 2 * d, lane));
+                ldsm4_t(pl, at_k(sP + kTile, 16 * i, 2 * d, lane));
+                mma(U[2 * d], oh[i], ph[0], ph[1]);
+                mma(U[2 * d + 1], oh[i], ph[2], ph[3]);
+                mma(U[2 * d], oh[i], pl[0], pl[1]);
+                mma(U[2 * d + 1], oh[i], pl[2], pl[3]);
+            }
+        }
+
+        // dY^T = dU^T T
+        float Y[8][4];
+#pragma unroll
+        for (int n = 0; n < 8; n++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) Y[n][e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            uint32_t uh[4], ul[4];
+            split_a(U[2 * i], U[2 * i + 1], uh, ul);
+#pragma unroll
+            for (int d = 0; d <= i; d++) {
+                uint32_t th[4], tl[4];
+                ldsm4_t(th, at_k(sT, 16 * i, 2 * d, lane));
+                ldsm4_t(tl, at_k(sT + kTile, 16 * i, 2 * d, lane));
+                mma(Y[2 * d], uh, th[0], th[1]);
+                mma(Y[2 * d + 1], uh, th[2], th[3]);
+                mma(Y[2 * d], ul, th[0], th[1]);
+                mma(Y[2 * d + 1], ul, th[2], th[3]);
+                mma(Y[2 * d], uh, tl[0], tl[1]);
+                mma(Y[2 * d + 1], uh, tl[2], tl[3]);
+            }
+        }
+        uint8_t* ky = a.kept.y + ((ch0 + c) * gridDim.x + slice) * (size_t)(2 * kTile);
+#pragma unroll
+        for (int n = 0; n < 8; n++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                uint32_t hi, lo;
+                split2(Y[n][2 * e], Y[n][2 * e + 1], hi, lo);
+                const uint32_t off = tile_at(0, 16 * w + g + 8 * e, n) + 4 * t;
+                *reinterpret_cast<uint32_t*>(ky + off) = hi;
+                *reinterpret_cast<uint32_t*>(ky + kTile + off) = lo;
+            }
+
+        // dS^T <- exp(G_C) dS^T + (exp(G) dO)^T Q - (exp(G) beta dY)^T K
+        const float eC = gt[C - 1];
+        uint32_t yh[4][4], yl[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const int n = 2 * i + j, tok = 8 * n + 2 * t;
+                const float2 eg = *reinterpret_cast<const float2*>(gt + tok);
+                const float2 bt = *reinterpret_cast<const float2*>(gt + 2 * C + tok);
+                Y[n][0] *= -eg.x * bt.x;
+                Y[n][1] *= -eg.y * bt.y;
+                Y[n][2] *= -eg.x * bt.x;
+                Y[n][3] *= -eg.y * bt.y;
+#pragma unroll
+                for (int r = 2 * j; r < 2 * j + 2; r++) {
+                    const uint32_t x = oh[i][r];
+                    split2(tc::bf16lo(x) * eg.x, tc::bf16hi(x) * eg.y, oh[i][r], ol[i][r]);
+                }
+            }
+            split_a(Y[2 * i], Y[2 * i + 1], yh[i], yl[i]);
+        }
+#pragma unroll
+        for (int d = 0; d < DK / 16; d++) {
+            float acc[2][2][4];
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) acc[0][i][e] = acc[1][i][e] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                uint32_t bq[4], bk[4];
+                ldsm4_t(bq, at_k(sQ, 16 * j, 2 * d, lane));
+                ldsm4_t(bk, at_k(sK, 16 * j, 2 * d, lane));
+                mma(acc[0][0], oh[j], bq[0], bq[1]);
+                mma(acc[0][1], oh[j], bq[2], bq[3]);
+                mma(acc[1][0], yh[j], bk[0], bk[1]);
+                mma(acc[1][1], yh[j], bk[2], bk[3]);
+                mma(acc[0][0], ol[j], bq[0], bq[1]);
+                mma(acc[0][1], ol[j], bq[2], bq[3]);
+                mma(acc[1][0], yl[j], bk[0], bk[1]);
+                mma(acc[1][1], yl[j], bk[2], bk[3]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    S[2 * d + i][e] = fmaf(eC, S[2 * d + i][e], acc[0][i][e] + acc[1][i][e]);
+        }
+        __syncwarp();
+        if (lane == 0) {
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(empty + st);
+        }
+    }
+    if (dinitial) {
+#pragma unroll
+        for (int n = 0; n < DK / 8; n++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int r = 8 * n + 2 * t + (e & 1), cc = col + 8 * (e >> 1);
+                if (cc < a.dv) dinitial[sb + (size_t)r * a.dv + cc] = S[n][e];
+            }
+    }
+}
+
+// ------------------------------------------------------------------ kernels
+
+template <int DK, int MODE>
+__global__ void __launch_bounds__(kChainThreads, 1)
+    k_delta_chain(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ ChainArgs a) {
+    chain_forward<DK, MODE>(mq, mk, mv, a, blockIdx.z);
+}
+
+// The backward's two chains do not depend on each other: half of the blocks
+// walk forward (states and corrections), half backward, side by side.
+template <int DK>
+__global__ void __launch_bounds__(kChainThreads, 1)
+    k_delta_chains(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
+                   const __grid_constant__ ChainArgs a, const float* dfinal, float* dinitial) {
+    if (blockIdx.z & 1) chain_forward<DK, kKeep>(mq, mk, mv, a, blockIdx.z >> 1);
+    else chain_backward<DK>(mq, mk, mo, a, dfinal, dinitial, blockIdx.z >> 1);
 }
 
 template <int DK>
-ret_status prep(const DeltaArgs& a, uint8_t* tiles, float* gates, cudaStream_t s) {
+ret_status prep(const DeltaArgs& a, uint8_t* tiles, uint8_t* gates, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(k_delta_prep<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, prep_smem<DK>());
     if (e != cudaSuccess) return fail(RET_ERR_CUDA, "delta rule tables: %s", cudaGetErrorString(e));
     const int nc = chunks_of(a.N);
@@ -574,7 +829,7 @@ ret_status chain_dk(const DeltaArgs& a, const ChainArgs& c, cudaStream_t s) {
     return a.dk == 64 ? chain<64, MODE>(a, c, s) : a.dk == 128 ? chain<128, MODE>(a, c, s) : chain<256, MODE>(a, c, s);
 }
 
-ChainArgs chain_args(const DeltaArgs& a, const uint8_t* tiles, const float* gates) {
+ChainArgs chain_args(const DeltaArgs& a, const uint8_t* tiles, const uint8_t* gates) {
     ChainArgs c{};
     c.tiles = tiles;
     c.gates = gates;
@@ -592,17 +847,29 @@ ChainArgs chain_args(const DeltaArgs& a, const uint8_t* tiles, const float* gate
 
 }  // namespace
 
-ret_status launch_prep(const DeltaArgs& a, uint8_t* tiles, float* gates, cudaStream_t s) {
+ret_status launch_prep(const DeltaArgs& a, uint8_t* tiles, uint8_t* gates, cudaStream_t s) {
     return a.dk == 64 ? prep<64>(a, tiles, gates, s) : a.dk == 128 ? prep<128>(a, tiles, gates, s) : prep<256>(a, tiles, gates, s);
 }
 
-ret_status launch_keep(const DeltaArgs& a, const uint8_t* tiles, const float* gates, uint8_t* keep_s, uint8_t* keep_u,
-                       cudaStream_t s) {
+template <int DK>
+static ret_status chains(const DeltaArgs& a, const ChainArgs& c, cudaStream_t s) {
+    CUtensorMap mq, mk, mv, mo;
+    if (!chunk_map(&mq, a.q, a.B, a.N, a.Hk, DK) || !chunk_map(&mk, a.k, a.B, a.N, a.Hk, DK) ||
+        !chunk_map(&mv, a.v, a.B, a.N, a.H, a.dv) || !chunk_map(&mo, a.dout, a.B, a.N, a.H, a.dv))
+        return RET_ERR_CUDA;
+    constexpr int smem = std::max(Stage<DK, kKeep>::smem, BackStage<DK>::smem);
+    cudaError_t e = cudaFuncSetAttribute(k_delta_chains<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return fail(RET_ERR_CUDA, "delta rule: %s", cudaGetErrorString(e));
+    k_delta_chains<DK><<<dim3(slices_of(a.dv), a.H, 2 * a.B), kChainThreads, smem, s>>>(mq, mk, mv, mo, c, a.dfinal_state,
+                                                                                      a.dinitial_state);
+    return check_launch("delta rule: the backward's chains");
+}
+
+ret_status launch_chains(const DeltaArgs& a, const uint8_t* tiles, const uint8_t* gates, const Kept& kept, cudaStream_t s) {
     ChainArgs c = chain_args(a, tiles, gates);
     c.final_state = nullptr;
-    c.keep_s = keep_s;
-    c.keep_u = keep_u;
-    return chain_dk<kKeep>(a, c, s);
+    c.kept = kept;
+    return a.dk == 64 ? chains<64>(a, c, s) : a.dk == 128 ? chains<128>(a, c, s) : chains<256>(a, c, s);
 }
 
 }  // namespace delta
@@ -614,13 +881,13 @@ bool delta_chunk_shape_ok(const DeltaArgs& a) {
 }
 
 size_t delta_forward_ws_bytes(const DeltaArgs& a) {
-    return (size_t)a.B * a.H * chunks_of(a.N) * (4 * kTile + kGates * 4);
+    return (size_t)a.B * a.H * chunks_of(a.N) * (4 * kTile + kGateRow);
 }
 
 ret_status launch_delta_forward(const DeltaArgs& a, void* ws, cudaStream_t s) {
     const size_t n = (size_t)a.B * a.H * chunks_of(a.N);
     uint8_t* tiles = reinterpret_cast<uint8_t*>(ws);
-    float* gates = reinterpret_cast<float*>(tiles + n * 4 * kTile);
+    uint8_t* gates = tiles + n * 4 * kTile;
     ret_status st = launch_prep(a, tiles, gates, s);
     if (st != RET_OK) return st;
     const ChainArgs c = chain_args(a, tiles, gates);

@@ -1023,6 +1023,54 @@ ret_status ret_delta_decode_step(const void* q, const void* k, const void* v, co
     return launch_delta_step(a, state, stream);
 }
 
+size_t ret_delta_backward_workspace_bytes(int B, int N, int Hk, int H, int dk, int dv, ret_dtype in_dt) {
+    if (B < 1 || N < 1 || Hk < 1 || H < 1 || dk < 1 || dv < 1 || H % Hk) return 0;
+    DeltaArgs a{};
+    a.B = B; a.N = N; a.Hk = Hk; a.H = H; a.dk = dk; a.dv = dv; a.in_dt = in_dt;
+    return delta_chunk_shape_ok(a) ? delta_backward_ws_bytes(a) : 0;
+}
+
+ret_status ret_delta_backward_chunkwise(const void* q, const void* k, const void* v, const float* g,
+                                        const float* beta, const void* dout, const int32_t* lengths,
+                                        const float* initial_state, const float* dfinal_state, int B, int N, int Hk,
+                                        int H, int dk, int dv, void* dq, void* dk_out, void* dv_out, float* dg,
+                                        float* dbeta, float* dinitial_state, cudaStream_t stream, ret_dtype in_dt,
+                                        ret_dtype grad_dt, void* workspace, size_t workspace_bytes) {
+    t_err[0] = 0;
+    const char* who = "ret_delta_backward_chunkwise";
+    DeltaArgs a{};
+    a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.lengths = lengths;
+    a.initial_state = initial_state;
+    a.dout = dout; a.dfinal_state = dfinal_state;
+    a.dq = dq; a.dkk = dk_out; a.dvv = dv_out; a.dg = dg; a.dbeta = dbeta; a.dinitial_state = dinitial_state;
+    a.grad_dt = grad_dt;
+    a.B = B; a.N = N; a.Hk = Hk; a.H = H; a.dk = dk; a.dv = dv; a.in_dt = in_dt; a.out_dt = in_dt;
+    ret_status st = check_delta(who, a);
+    if (st != RET_OK) return st;
+    if (!dout || !dq || !dk_out || !dv_out || !dg || !dbeta)
+        return fail(RET_ERR_INVALID_ARG, "%s: NULL dout, dq, dk, dv, dg or dbeta", who);
+    if (!is_dtype(grad_dt)) return fail(RET_ERR_INVALID_ARG, "%s: unknown dtype", who);
+    if (B > 32767) return fail(RET_ERR_INVALID_ARG, "%s: at most 32767 sequences", who);
+    for (const void* p : {dout, (const void*)dfinal_state, (const void*)dq, (const void*)dk_out, (const void*)dv_out,
+                          (const void*)dg, (const void*)dbeta, (const void*)dinitial_state})
+        if (!aligned(p, 16)) return fail(RET_ERR_INVALID_ARG, "%s: dout and the gradients must be 16-byte aligned", who);
+    if (!delta_chunk_shape_ok(a))
+        return fail(RET_ERR_UNSUPPORTED, "%s: needs bf16 inputs, dk 64, 128 or 256 and dv a multiple of 8", who);
+    const size_t need = delta_backward_ws_bytes(a);
+    if ((st = check_workspace_buf(who, workspace, workspace_bytes, need)) != RET_OK) return st;
+    const size_t tok = (size_t)B * N, eq = tok * Hk * dk, ev = tok * H * dv, ng = tok * H * 4;
+    const size_t ns = (size_t)B * H * dk * dv * 4, ge = esize(grad_dt);
+    const Buf bufs[] = {{"q", q, eq * 2, false}, {"k", k, eq * 2, false}, {"v", v, ev * 2, false},
+                        {"g", g, ng, false}, {"beta", beta, ng, false}, {"dout", dout, ev * 2, false},
+                        {"lengths", lengths, (size_t)B * 4, false}, {"initial_state", initial_state, ns, false},
+                        {"dfinal_state", dfinal_state, ns, false}, {"dq", dq, eq * ge, true},
+                        {"dk", dk_out, eq * ge, true}, {"dv", dv_out, ev * ge, true}, {"dg", dg, ng, true},
+                        {"dbeta", dbeta, ng, true}, {"dinitial_state", dinitial_state, ns, true},
+                        {"workspace", workspace, need, true}};
+    if ((st = check_apart(who, bufs, 16)) != RET_OK) return st;
+    return launch_delta_backward(a, workspace, stream);
+}
+
 ret_status ret_selftest_bounded_wait(uint32_t polls, cudaStream_t stream) {
     t_err[0] = 0;
     if (polls < 1 || polls > (1u << 24))
@@ -1034,12 +1082,13 @@ ret_status ret_check_device_error(cudaStream_t stream) {
     t_err[0] = 0;
     cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return fail(RET_ERR_CUDA, "ret_check_device_error: %s", cudaGetErrorString(e));
-    int flag = 0, flag2 = 0, flag3 = 0;
+    int flag = 0, flag2 = 0, flag3 = 0, flag4 = 0;
     e = read_clear_error_chunk_ws(&flag);
     if (e == cudaSuccess) e = read_clear_error_gemm(&flag2);
     if (e == cudaSuccess) e = read_clear_error_delta(&flag3);
+    if (e == cudaSuccess) e = read_clear_error_delta_grads(&flag4);
     if (e != cudaSuccess) return fail(RET_ERR_CUDA, "ret_check_device_error: %s", cudaGetErrorString(e));
-    flag |= flag2 | flag3;
+    flag |= flag2 | flag3 | flag4;
     if (flag) return fail(RET_ERR_TIMEOUT, "a kernel gave up a bounded wait (device error word %d)", flag);
     return RET_OK;
 }
