@@ -148,7 +148,7 @@ def _ptr(t: Optional[torch.Tensor], name: str):
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 F32 = (torch.float32,)
@@ -161,7 +161,7 @@ def _buf(t: Optional[torch.Tensor], name: str, shape, dtypes, like: torch.Tensor
     cannot check either."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {list(shape)} (got {list(t.shape)})")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)} (got {t.dtype})")
@@ -604,19 +604,41 @@ def _call(like: torch.Tensor, stream, fn, *args):
     ``_STREAM`` stands for the stream (default: that device's current one)."""
     if not like.is_cuda:
         raise ValueError("the inputs must be CUDA tensors")
-    dev = like.device.index
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    s = _stream(stream)
+    dev = like.get_device()
+    # the plain handle: making a Stream object costs as much as a launch
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
     args = [s if a is _STREAM else a for a in args]
-    if dev == torch.cuda.current_device():
-        _check(fn(*args))
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args))
+            status = fn(*args)
+    if status != RET_OK:
+        _check(status)
+
+
+def _workspace(workspace, need: int, like: torch.Tensor, stream):
+    """(pointer, bytes) of the caller's workspace, or of a new one, and the
+    tensor that holds it.  A new one belongs to the stream of the call: it is
+    free again when the call returns, before its kernels have run."""
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        if stream is None:
+            workspace = like.new_empty((need,), dtype=torch.uint8)
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+            with torch.cuda.stream(stream):
+                workspace = like.new_empty((need,), dtype=torch.uint8)
+    else:
+        _same_device(like, workspace=workspace)
+    return _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace
 
 
 _STREAM = object()
+_CODES = {torch.float32: RET_F32, torch.bfloat16: RET_BF16}
+_Strides = ctypes.c_int64 * 3
 
 _ROTARY_LAYOUTS = {"interleaved": 0, "half": 1}
 _ROTARY_SCALINGS = {"none": 0, "linear": 1, "yarn": 2}
@@ -643,9 +665,11 @@ def _rotary_view(t: Optional[torch.Tensor], name: str):
         return None, None
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if t.is_contiguous():
+        return t.data_ptr(), None
     if t.stride(3) != 1 and t.shape[3] > 1:
         raise ValueError(f"the components of {name} must be consecutive (stride {t.stride(3)})")
-    return ctypes.c_void_p(t.data_ptr()), (ctypes.c_int64 * 3)(*t.stride()[:3])
+    return t.data_ptr(), _Strides(*t.stride()[:3])
 
 
 def ret_rotary(q, k=None, freqs=None, positions=None, pos_offset: int = 0, layout: str = "interleaved",
@@ -677,29 +701,33 @@ def ret_rotary(q, k=None, freqs=None, positions=None, pos_offset: int = 0, layou
         raise ValueError("freqs must be a contiguous float64 vector on the CPU")
     if rotary_dim is not None and 2 * freqs.numel() != rotary_dim:
         raise ValueError(f"freqs has {freqs.numel()} entries, expected {rotary_dim // 2}")
-    q_out = torch.empty((B, N, H, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
-    if k is not None and k_out is None:
-        k_out = torch.empty((B, N, Hk, d), dtype=q.dtype, device=q.device)
-    _buf(q_out, "q_out", (B, N, H, d), (q.dtype,), q)
-    _buf(k_out, "k_out", (B, N, Hk, d), (q.dtype,), q)
+    if q_out is None:
+        q_out = q.new_empty((B, N, H, d))
+    else:
+        _buf(q_out, "q_out", (B, N, H, d), (q.dtype,), q)
+    if k is not None:
+        _same_device(q, k=k)
+        if k_out is None:
+            k_out = q.new_empty((B, N, Hk, d))
+        else:
+            _buf(k_out, "k_out", (B, N, Hk, d), (q.dtype,), q)
     _buf(positions, "positions", (B, N), (torch.int64,), q)
-    _same_device(q, k=k)
     (qp, qs), (kp, ks) = _rotary_view(q, "q"), _rotary_view(k, "k")
     (qop, qos), (kop, kos) = _rotary_view(q_out, "q_out"), _rotary_view(k_out, "k_out")
-    _call(q, stream, lib.ret_rotary, qp, kp, qop, kop, qs, ks, qos, kos, ctypes.c_void_p(freqs.data_ptr()),
+    _call(q, stream, lib.ret_rotary, qp, kp, qop, kop, qs, ks, qos, kos, freqs.data_ptr(),
           float(scale), _ptr(positions, "positions"), int(pos_offset), int(bool(inverse)), _ROTARY_LAYOUTS[layout],
           B, N, H, Hk, d, 2 * freqs.numel(), _dt(q.dtype), _STREAM)
     return q_out if k is None else (q_out, k_out)
 
 
-def _weight_dt(x, d, **weights):
-    """dtype code of the layer norm's weights (fp32 or bf16, the same for all)."""
-    given = [t for t in weights.values() if t is not None]
-    for name, t in weights.items():
-        _buf(t, name, (d,), FLOATS, x)
-    if any(t.dtype != given[0].dtype for t in given):
+def _weight_dt(x, d, gain, bias=None):
+    """dtype code of the layer norm's weights (fp32 or bf16, the same for both)."""
+    _buf(gain, "gain", (d,), FLOATS, x)
+    _buf(bias, "bias", (d,), FLOATS, x)
+    if gain is not None and bias is not None and gain.dtype != bias.dtype:
         raise TypeError("gain and bias must share a dtype")
-    return _dt(given[0].dtype) if given else RET_F32
+    given = bias if gain is None else gain
+    return RET_F32 if given is None else _CODES[given.dtype]
 
 
 def ret_layernorm_forward(x, gain=None, bias=None, eps: float = 1e-5, out=None, mean=None, rstd=None,
@@ -711,14 +739,16 @@ def ret_layernorm_forward(x, gain=None, bias=None, eps: float = 1e-5, out=None, 
         raise ValueError("x must be [..., d] with at least one row")
     d, lead = x.shape[-1], x.shape[:-1]
     rows = x.numel() // d
-    w = _weight_dt(x, d, gain=gain, bias=bias)
-    out = torch.empty_like(x) if out is None else out
-    if want_stats:
-        mean = torch.empty(lead, dtype=torch.float32, device=x.device) if mean is None else mean
-        rstd = torch.empty(lead, dtype=torch.float32, device=x.device) if rstd is None else rstd
-    _buf(out, "out", x.shape, (x.dtype,), x)
+    w = _weight_dt(x, d, gain, bias)
+    if out is None:
+        out = x.new_empty(x.shape)
+    else:
+        _buf(out, "out", x.shape, (x.dtype,), x)
     _buf(mean, "mean", lead, F32, x)
     _buf(rstd, "rstd", lead, F32, x)
+    if want_stats:
+        mean = x.new_empty(lead, dtype=torch.float32) if mean is None else mean
+        rstd = x.new_empty(lead, dtype=torch.float32) if rstd is None else rstd
     _call(x, stream, lib.ret_layernorm_forward, _ptr(x, "x"), _ptr(gain, "gain"), _ptr(bias, "bias"), float(eps), rows,
           d, _ptr(out, "out"), _ptr(mean, "mean"), _ptr(rstd, "rstd"), _dt(x.dtype), w, _STREAM)
     return (out, mean, rstd) if mean is not None or rstd is not None else out
@@ -738,25 +768,25 @@ def ret_layernorm_backward(dout, x, mean, rstd, gain=None, dx=None, dgain=None, 
         raise ValueError("x must be [..., d] with at least one row")
     d, lead = x.shape[-1], x.shape[:-1]
     rows = x.numel() // d
-    w = _weight_dt(x, d, gain=gain)
-    dx = torch.empty_like(x) if dx is None else dx
-    if want_weights:
-        dgain = torch.empty(d, dtype=torch.float32, device=x.device) if dgain is None else dgain
-        dbias = torch.empty(d, dtype=torch.float32, device=x.device) if dbias is None else dbias
+    w = _weight_dt(x, d, gain)
     _buf(dout, "dout", x.shape, (x.dtype,), x)
-    _buf(dx, "dx", x.shape, (x.dtype,), x)
     _buf(mean, "mean", lead, F32, x)
     _buf(rstd, "rstd", lead, F32, x)
     _buf(dgain, "dgain", (d,), F32, x)
     _buf(dbias, "dbias", (d,), F32, x)
-    if workspace is None and (dgain is not None or dbias is not None):
-        workspace = torch.empty(max(ret_layernorm_backward_workspace_bytes(rows, d), 1), dtype=torch.uint8,
-                                device=x.device)
-    _same_device(x, workspace=workspace)
-    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    if dx is None:
+        dx = x.new_empty(x.shape)
+    else:
+        _buf(dx, "dx", x.shape, (x.dtype,), x)
+    if want_weights:
+        dgain = x.new_empty((d,), dtype=torch.float32) if dgain is None else dgain
+        dbias = x.new_empty((d,), dtype=torch.float32) if dbias is None else dbias
+    wanted = workspace is None and (dgain is not None or dbias is not None)
+    need = lib.ret_layernorm_backward_workspace_bytes(rows, d) if wanted else 0
+    wp, nbytes, workspace = _workspace(workspace, need, x, stream)
     _call(x, stream, lib.ret_layernorm_backward, _ptr(dout, "dout"), _ptr(x, "x"), _ptr(mean, "mean"),
           _ptr(rstd, "rstd"), _ptr(gain, "gain"), rows, d, _ptr(dx, "dx"), _ptr(dgain, "dgain"), _ptr(dbias, "dbias"),
-          _dt(x.dtype), w, _ptr(workspace, "workspace"), nbytes, _STREAM)
+          _dt(x.dtype), w, wp, nbytes, _STREAM)
     return dx, dgain, dbias
 
 
@@ -770,8 +800,9 @@ def _delta_shapes(q, k, v, g, beta, n_lead: int):
         raise TypeError("q, k and v must share a dtype")
     _same_device(q, k=k, v=v)
     H, dv = v.shape[n_lead:]
-    _buf(g, "g", (*lead, H), F32, q)
-    _buf(beta, "beta", (*lead, H), F32, q)
+    gates = (*lead, H)
+    _buf(g, "g", gates, F32, q)
+    _buf(beta, "beta", gates, F32, q)
     Hk, dk = q.shape[n_lead:]
     return lead, Hk, H, dk, dv
 
@@ -789,21 +820,17 @@ def ret_delta_forward_chunkwise(q, k, v, g, beta, lengths=None, initial_state=No
     (rows behind a sequence's end are not written), or ``(out, final_state)``
     when a final state is requested (passed in or ``want_final_state``)."""
     (B, N), Hk, H, dk, dv = _delta_shapes(q, k, v, g, beta, 2)
-    if out is None:
-        out = torch.empty((B, N, H, dv), dtype=out_dtype or q.dtype, device=q.device)
-    if final_state is None and want_final_state:
-        final_state = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
     _seq_outputs(q, out, final_state, B, N, H, dk, dv, initial_state)
     _buf(lengths, "lengths", (B,), (torch.int32,), q)
-    if workspace is None:
-        nb = ret_delta_workspace_bytes(B, N, Hk, H, dk, dv, q.dtype)
-        workspace = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
-    _same_device(q, workspace=workspace)
-    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    if out is None:
+        out = q.new_empty((B, N, H, dv), dtype=out_dtype or q.dtype)
+    if final_state is None and want_final_state:
+        final_state = q.new_empty((B, H, dk, dv), dtype=torch.float32)
+    need = lib.ret_delta_workspace_bytes(B, N, Hk, H, dk, dv, _dt(q.dtype)) if workspace is None else 0
+    wp, nbytes, workspace = _workspace(workspace, need, q, stream)
     _call(q, stream, lib.ret_delta_forward_chunkwise, _ptr(q, "q"), _ptr(k, "k"), _ptr(v, "v"), _ptr(g, "g"),
           _ptr(beta, "beta"), _ptr(lengths, "lengths"), _ptr(initial_state, "initial_state"), B, N, Hk, H, dk, dv,
-          _ptr(out, "out"), _ptr(final_state, "final_state"), _STREAM, _dt(q.dtype), _dt(out.dtype),
-          _ptr(workspace, "workspace"), nbytes)
+          _ptr(out, "out"), _ptr(final_state, "final_state"), _STREAM, _dt(q.dtype), _dt(out.dtype), wp, nbytes)
     return (out, final_state) if final_state is not None else out
 
 
@@ -816,8 +843,9 @@ def ret_delta_decode_step(q, k, v, g, beta, state, out=None, out_dtype=None, str
         raise ValueError("state must be float32 [B, H, dk, dv]")
     _buf(state, "state", (B, H, dk, dv), F32, q)
     if out is None:
-        out = torch.empty((B, H, dv), dtype=out_dtype or torch.float32, device=q.device)
-    _buf(out, "out", (B, H, dv), FLOATS, q)
+        out = q.new_empty((B, H, dv), dtype=out_dtype or torch.float32)
+    else:
+        _buf(out, "out", (B, H, dv), FLOATS, q)
     _call(q, stream, lib.ret_delta_decode_step, _ptr(q, "q"), _ptr(k, "k"), _ptr(v, "v"), _ptr(g, "g"),
           _ptr(beta, "beta"), _ptr(state, "state"), _ptr(out, "out"), _STREAM, B, Hk, H, dk, dv, _dt(q.dtype),
           _dt(out.dtype))
@@ -842,27 +870,24 @@ def ret_delta_backward_chunkwise(q, k, v, g, beta, dout, lengths=None, initial_s
     _buf(initial_state, "initial_state", (B, H, dk_, dv_), F32, q)
     _buf(dfinal_state, "dfinal_state", (B, H, dk_, dv_), F32, q)
     _buf(lengths, "lengths", (B,), (torch.int32,), q)
-    dq = torch.empty((B, N, Hk, dk_), dtype=grad_dtype, device=q.device) if dq is None else dq
-    dk = torch.empty((B, N, Hk, dk_), dtype=dq.dtype, device=q.device) if dk is None else dk
-    dv = torch.empty((B, N, H, dv_), dtype=dq.dtype, device=q.device) if dv is None else dv
-    dg = torch.empty((B, N, H), dtype=torch.float32, device=q.device) if dg is None else dg
-    dbeta = torch.empty((B, N, H), dtype=torch.float32, device=q.device) if dbeta is None else dbeta
-    if dinitial_state is None and (initial_state is not None if want_dinitial_state is None else want_dinitial_state):
-        dinitial_state = torch.empty((B, H, dk_, dv_), dtype=torch.float32, device=q.device)
+    dq = q.new_empty((B, N, Hk, dk_), dtype=grad_dtype) if dq is None else dq
     _buf(dq, "dq", (B, N, Hk, dk_), FLOATS, q)
     _buf(dk, "dk", (B, N, Hk, dk_), (dq.dtype,), q)
     _buf(dv, "dv", (B, N, H, dv_), (dq.dtype,), q)
     _buf(dg, "dg", (B, N, H), F32, q)
     _buf(dbeta, "dbeta", (B, N, H), F32, q)
     _buf(dinitial_state, "dinitial_state", (B, H, dk_, dv_), F32, q)
-    if workspace is None:
-        nb = ret_delta_backward_workspace_bytes(B, N, Hk, H, dk_, dv_, q.dtype)
-        workspace = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
-    _same_device(q, workspace=workspace)
-    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    dk = dq.new_empty((B, N, Hk, dk_)) if dk is None else dk
+    dv = dq.new_empty((B, N, H, dv_)) if dv is None else dv
+    dg = q.new_empty((B, N, H), dtype=torch.float32) if dg is None else dg
+    dbeta = q.new_empty((B, N, H), dtype=torch.float32) if dbeta is None else dbeta
+    if dinitial_state is None and (initial_state is not None if want_dinitial_state is None else want_dinitial_state):
+        dinitial_state = q.new_empty((B, H, dk_, dv_), dtype=torch.float32)
+    need = lib.ret_delta_backward_workspace_bytes(B, N, Hk, H, dk_, dv_, _dt(q.dtype)) if workspace is None else 0
+    wp, nbytes, workspace = _workspace(workspace, need, q, stream)
     _call(q, stream, lib.ret_delta_backward_chunkwise, _ptr(q, "q"), _ptr(k, "k"), _ptr(v, "v"), _ptr(g, "g"),
           _ptr(beta, "beta"), _ptr(dout, "dout"), _ptr(lengths, "lengths"), _ptr(initial_state, "initial_state"),
           _ptr(dfinal_state, "dfinal_state"), B, N, Hk, H, dk_, dv_, _ptr(dq, "dq"), _ptr(dk, "dk"), _ptr(dv, "dv"),
           _ptr(dg, "dg"), _ptr(dbeta, "dbeta"), _ptr(dinitial_state, "dinitial_state"), _STREAM, _dt(q.dtype),
-          _dt(dq.dtype), _ptr(workspace, "workspace"), nbytes)
+          _dt(dq.dtype), wp, nbytes)
     return dq, dk, dv, dg, dbeta, dinitial_state

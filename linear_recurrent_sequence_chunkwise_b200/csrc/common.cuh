@@ -45,6 +45,7 @@ constexpr int kErrTimeout = 1;
 cudaError_t read_clear_error_chunk_ws(int* flag);
 cudaError_t read_clear_error_delta(int* flag);
 cudaError_t read_clear_error_delta_grads(int* flag);
+cudaError_t read_clear_error_delta_step(int* flag);
 
 // ---------------------------------------------------------------- device side
 

@@ -3,18 +3,23 @@
 //     with h = (x - mean) rstd and t = dy gain:
 //     dx = rstd (t - avg(t) - h avg(t h)),  dgain = sum_rows dy h,  dbias = sum_rows dy
 //
-// Bound by memory: x (and dy) are read once and y (dx) written once.  A row is
-// held in the registers of a group of T threads, the smallest power of two
-// (32 to 1,024) whose 16-byte vectors cover it; a group of one warp needs no
-// barrier, a larger one a named barrier of its own, so the groups of a block
-// run apart.  The forward takes the variance about the mean (two reductions),
+// The bytes (x, dy read once, y, dx written once) are the floor, the
+// instructions are close behind: on 2,048 bf16 columns a sum over the threads
+// of a row costs a warp as much as eight elements of each of its lanes.  So a
+// row belongs to as few threads as its registers allow: the forward gives a
+// lane 32 elements and its next row's loads, the backward 16 (it holds the row's two inputs, the weights and two
+// columns' sums), a row in a group of 32 to 512 threads with a named barrier
+// of its own.  The forward takes the variance about the mean (two reductions),
 // which keeps rows with a large mean exact.
 //
-// The backward's column sums: a group walks many rows and keeps its columns'
-// partial sums of dgain and dbias in registers, the groups of a block add
-// theirs in shared memory, every block writes one partial row, and a second
-// kernel adds those in a fixed order (the result does not depend on timing).
-// All sums are fp32.
+// The backward's column sums: a group walks many rows, the next one's loads in
+// flight, and keeps its columns' partial sums of dgain and dbias in registers;
+// the groups of a block add theirs in shared memory, every block writes one
+// partial row, and a second kernel adds those in a fixed order (the result
+// does not depend on timing).  All sums are fp32.
+//
+// 8192 x 2048 bf16: forward %F%, backward %B% (with 8 elements in a lane and
+// eight warps a row: 28 and 39 us).
 #include <algorithm>
 
 #include "kernels.h"
@@ -23,21 +28,35 @@ namespace ret {
 
 namespace {
 
+constexpr int kBwdElems = 16;    // elements of a row in a thread of the backward
+constexpr int kBwdMost = 512;    // threads of a block of the backward
+constexpr int kBwdBlocks = 296;  // most blocks of the backward, and so partial rows
+constexpr int kSms = 148;
+
 __device__ __forceinline__ float f_of(float x) { return x; }
 __device__ __forceinline__ float f_of(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// VEC consecutive elements as fp32; VEC * sizeof(T) is 16 (aligned) or VEC is 1.
+// VEC consecutive elements as they lie in memory; VEC * sizeof(T) is 16
+// (aligned) or VEC is 1.  A load behind the row's end reads the row's last
+// elements instead and is cleared where it is used: a branch around a load
+// would wait for the load (8,192 x 2,048 forward: %BR% with branches).
 template <typename T, int VEC>
-__device__ __forceinline__ void ld_vec(const T* p, float* f) {
-    if constexpr (VEC == 1) {
-        f[0] = f_of(p[0]);
-    } else {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        const T* e = reinterpret_cast<const T*>(&u);
-#pragma unroll
-        for (int i = 0; i < VEC; i++) f[i] = f_of(e[i]);
+struct alignas(VEC == 1 ? sizeof(T) : 16) Raw {
+    T e[VEC];
+    __device__ __forceinline__ void keep_if(bool in) {
+        if constexpr (VEC == 1) {
+            if (!in) st_from_float(e, 0, 0.f);
+        } else {
+            uint4& u = *reinterpret_cast<uint4*>(e);
+            if (!in) u = make_uint4(0, 0, 0, 0);
+        }
     }
-}
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (VEC == 1) e[0] = p[0];
+        else *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
+    }
+    __device__ __forceinline__ float operator[](int i) const { return f_of(e[i]); }
+};
 template <typename T, int VEC>
 __device__ __forceinline__ void st_vec(T* p, const float* f) {
     if constexpr (VEC == 1) {
@@ -50,169 +69,258 @@ __device__ __forceinline__ void st_vec(T* p, const float* f) {
         *reinterpret_cast<uint4*>(p) = u;
     }
 }
-// VEC weights at column c (their own dtype; not necessarily 16-byte wide).
+// VEC weights at column c, in their own dtype (kept so in registers).
 template <typename W, int VEC>
-__device__ __forceinline__ void ld_w(const W* w, int c, float* f) {
+__device__ __forceinline__ void ld_w(const W* w, int c, W* f) {
     if constexpr (VEC * sizeof(W) >= 16) {
 #pragma unroll
-        for (int i = 0; i < VEC; i += 16 / (int)sizeof(W)) ld_vec<W, 16 / (int)sizeof(W)>(w + c + i, f + i);
+        for (int i = 0; i < VEC; i += 16 / (int)sizeof(W))
+            *reinterpret_cast<uint4*>(f + i) = *reinterpret_cast<const uint4*>(w + c + i);
     } else {
 #pragma unroll
-        for (int i = 0; i < VEC; i++) f[i] = f_of(w[c + i]);
+        for (int i = 0; i < VEC; i++) f[i] = w[c + i];
     }
 }
 
-// Sum over the T threads of a group; every thread gets it.  `red`: the
-// group's 32 words, alternating between two halves so that one barrier per
-// sum is enough.
+// Sums over the T threads of a group; every thread gets them.  `red`: words of
+// the group, alternating between two halves so that one barrier per sum is
+// enough.
 struct GroupSum {
-    float2* red;  // [2][T / 32]
+    float* red;  // [2][2 T / 32]
     int T, bar, half;
-    __device__ __forceinline__ float2 operator()(float2 x) {
+    __device__ __forceinline__ float one(float x) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
-            x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
-        }
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (T == 32) return x;
-        const int nw = T / 32, w = (threadIdx.x % T) >> 5;
-        float2* r = red + half * nw;
-        half ^= 1;
-        if ((threadIdx.x & 31) == 0) r[w] = x;
-        asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(T) : "memory");
-        float2 s = r[0];
-        for (int i = 1; i < nw; i++) {
-            s.x += r[i].x;
-            s.y += r[i].y;
-        }
-        return s;
+        const int nw = T / 32;
+        float* r = next(nw);
+        if ((threadIdx.x & 31) == 0) r[(threadIdx.x % T) >> 5] = x;
+        sync();
+        x = r[0];
+        for (int i = 1; i < nw; i++) x += r[i];
+        return x;
     }
+    // Two sums: half of the lanes goes on with each.
+    __device__ __forceinline__ float2 two(float x, float y) {
+        const bool up = threadIdx.x & 16;
+        float s = (up ? y : x) + __shfl_xor_sync(0xffffffffu, up ? x : y, 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (T == 32) {
+            const float other = __shfl_xor_sync(0xffffffffu, s, 16);
+            return up ? make_float2(other, s) : make_float2(s, other);
+        }
+        const int nw = T / 32;
+        float* r = next(nw);
+        if ((threadIdx.x & 15) == 0) r[(threadIdx.x % T) >> 4] = s;
+        sync();
+        float2 t = *reinterpret_cast<const float2*>(r);
+        for (int i = 1; i < nw; i++) {
+            const float2 u = *reinterpret_cast<const float2*>(r + 2 * i);
+            t.x += u.x;
+            t.y += u.y;
+        }
+        return t;
+    }
+    __device__ __forceinline__ float* next(int nw) {
+        float* r = red + half * 2 * nw;
+        half ^= 1;
+        return r;
+    }
+    __device__ __forceinline__ void sync() { asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(T) : "memory"); }
 };
 
-template <typename T, typename W, int VEC, int NV>
-__global__ void __launch_bounds__(1024) k_ln_forward(const T* __restrict__ x, const W* __restrict__ gain,
-                                                    const W* __restrict__ bias, T* __restrict__ y,
-                                                    float* __restrict__ mean_out, float* __restrict__ rstd_out,
-                                                    long long rows, int d, float eps, int group) {
-    __shared__ float2 red[64];
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ unsigned long long u64(float2 x) { return *reinterpret_cast<unsigned long long*>(&x); }
+__device__ __forceinline__ float2 f2(unsigned long long x) { return *reinterpret_cast<float2*>(&x); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)), "l"(u64(c)));
+    return f2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)));
+    return f2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(u64(a)), "l"(u64(b)));
+    return f2(r);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// FULL: the group's loads cover the row exactly and both weights are given.
+template <typename T, typename W, int VEC, int NV, bool FULL>
+__global__ void __launch_bounds__(512) k_ln_forward(const T* __restrict__ x, const W* __restrict__ gain,
+                                                   const W* __restrict__ bias, T* __restrict__ y,
+                                                   float* __restrict__ mean_out, float* __restrict__ rstd_out,
+                                                   long long rows, int d, float eps, int group) {
+    constexpr int P = VEC * NV / 2;
+    __shared__ float red[64];
     const int gi = threadIdx.x / group, lane = threadIdx.x % group, ng = blockDim.x / group;
-    const long long row = (long long)blockIdx.x * ng + gi;
-    if (row >= rows) return;  // the whole group
-    GroupSum sum{red + gi * 2 * (group / 32), group, 1 + gi, 0};
-    const T* xr = x + row * d;
-    float f[NV][VEC];
-    float s = 0.f;
+    GroupSum sum{red + gi * 4 * (group / 32), group, 1 + gi, 0};
+    const float inv_d = 1.f / d;
+    const long long stride = (long long)gridDim.x * ng;
+    Raw<T, VEC> raw[NV];
+    auto load = [&](long long r) {
+        const T* xr = x + min(r, rows - 1) * d;
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const int c = (i * group + lane) * VEC;
-        if (c < d) {
-            ld_vec<T, VEC>(xr + c, f[i]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < VEC; e++) f[i][e] = 0.f;
+        for (int i = 0; i < NV; i++) {
+            const int c = (i * group + lane) * VEC;
+            raw[i].load(xr + (FULL ? c : min(c, d - VEC)));
         }
-    }
+    };
+    long long row = (long long)blockIdx.x * ng + gi;
+    load(row);
+    for (; row < rows; row += stride) {
+        float2 f[P], s = both(0.f), v = s;
 #pragma unroll
-    for (int i = 0; i < NV; i++)
-#pragma unroll
-        for (int e = 0; e < VEC; e++) s += f[i][e];
-    const float mean = sum(make_float2(s, 0.f)).x / d;
-    float v = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; i++)
-        if ((i * group + lane) * VEC < d) {
-#pragma unroll
-            for (int e = 0; e < VEC; e++) {
-                f[i][e] -= mean;
-                v = fmaf(f[i][e], f[i][e], v);
+        for (int p = 0; p < P; p++) {
+            f[p] = make_float2(raw[2 * p / VEC][2 * p % VEC], raw[(2 * p + 1) / VEC][(2 * p + 1) % VEC]);
+            if (!FULL) {
+                if ((2 * p / VEC * group + lane) * VEC >= d) f[p].x = 0.f;
+                if (((2 * p + 1) / VEC * group + lane) * VEC >= d) f[p].y = 0.f;
             }
+            s = add2(s, f[p]);
         }
-    const float rstd = 1.f / sqrtf(sum(make_float2(v, 0.f)).x / d + eps);
-    if (lane == 0) {
-        if (mean_out) mean_out[row] = mean;
-        if (rstd_out) rstd_out[row] = rstd;
-    }
+        load(row + stride);
+        const float mean = sum.one(s.x + s.y) * inv_d;
+        const float2 m2 = both(-mean);
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const int c = (i * group + lane) * VEC;
-        if (c >= d) continue;
-        float g[VEC], b[VEC];
-        if (gain) ld_w<W, VEC>(gain, c, g);
-        if (bias) ld_w<W, VEC>(bias, c, b);
-#pragma unroll
-        for (int e = 0; e < VEC; e++) {
-            float t = f[i][e] * rstd;
-            if (gain) t *= g[e];
-            if (bias) t += b[e];
-            f[i][e] = t;
+        for (int p = 0; p < P; p++) {
+            f[p] = add2(f[p], m2);
+            if (!FULL) {  // behind the row's end: no distance
+                if ((2 * p / VEC * group + lane) * VEC >= d) f[p].x = 0.f;
+                if (((2 * p + 1) / VEC * group + lane) * VEC >= d) f[p].y = 0.f;
+            }
+            v = fma2(f[p], f[p], v);
         }
-        st_vec<T, VEC>(y + row * d + c, f[i]);
+        const float rstd = 1.f / sqrtf(sum.one(v.x + v.y) * inv_d + eps);
+        if (lane == 0) {
+            if (mean_out) mean_out[row] = mean;
+            if (rstd_out) rstd_out[row] = rstd;
+        }
+        const float2 r2 = both(rstd);
+#pragma unroll
+        for (int p = 0; p < P; p++) f[p] = mul2(f[p], r2);
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = (i * group + lane) * VEC, at = FULL ? c : min(c, d - VEC);
+            alignas(16) W g[VEC], b[VEC];
+            if (FULL || gain) ld_w<W, VEC>(gain, at, g);
+            if (FULL || bias) ld_w<W, VEC>(bias, at, b);
+            float t[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; e += 2) {
+                if (FULL && VEC > 1) {
+                    const float2 u = fma2(f[(i * VEC + e) / 2], make_float2(f_of(g[e]), f_of(g[(e + 1) % VEC])),
+                                          make_float2(f_of(b[e]), f_of(b[(e + 1) % VEC])));
+                    t[e] = u.x;
+                    t[(e + 1) % VEC] = u.y;
+                } else {
+#pragma unroll
+                    for (int k = e; k < VEC && k < e + 2; k++) {
+                        const int j = i * VEC + k;
+                        t[k] = j & 1 ? f[j / 2].y : f[j / 2].x;
+                        if (gain) t[k] *= f_of(g[k]);
+                        if (bias) t[k] += f_of(b[k]);
+                    }
+                }
+            }
+            if (FULL || c < d) st_vec<T, VEC>(y + row * d + c, t);
+        }
     }
 }
 
 // part: [gridDim.x][2][d] column sums of each block, or null.
-template <typename T, typename W, int VEC, int NV>
-__global__ void __launch_bounds__(512) k_ln_backward(const T* __restrict__ dy, const T* __restrict__ x,
-                                                    const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
-                                                    const W* __restrict__ gain, T* __restrict__ dx,
-                                                    float* __restrict__ part, long long rows, int d, int group) {
-    __shared__ float2 red[32];
-    extern __shared__ float cols[];  // [2][group * NV * VEC]: the block's column sums
+// FULL: the group's loads cover the row exactly and a gain is given.
+template <typename T, typename W, int VEC, int NV, bool FULL>
+__global__ void __launch_bounds__(kBwdMost) k_ln_backward(const T* __restrict__ dy, const T* __restrict__ x,
+                                                         const float* __restrict__ mean_in,
+                                                         const float* __restrict__ rstd_in, const W* __restrict__ gain,
+                                                         T* __restrict__ dx, float* __restrict__ part, long long rows,
+                                                         int d, int group) {
+    constexpr int E = VEC * NV, P = E / 2;
+    // the next row's loads in flight, where they fit the registers
+    constexpr bool kAhead = FULL && sizeof(T) == 2;
+    __shared__ __align__(8) float red[64];
+    extern __shared__ float cols[];  // [2][group * E]: the block's column sums
     const int gi = threadIdx.x / group, lane = threadIdx.x % group, ng = blockDim.x / group;
-    GroupSum sum{red + gi * 2 * (group / 32), group, 1 + gi, 0};
-    float g[NV][VEC], ag[NV][VEC], ab[NV][VEC];
+    GroupSum sum{red + gi * 4 * (group / 32), group, 1 + gi, 0};
+    const long long stride = (long long)gridDim.x * ng;
+    long long row = (long long)blockIdx.x * ng + gi;
+    // element e of the thread: column ((e / VEC) * group + lane) * VEC + e % VEC
+    alignas(16) W g[NV][VEC];
+    float2 ag[P], ab[P];
+    Raw<T, VEC> nx[NV], ny[NV];
+    float nm = 0.f, nr = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; i++)
+#pragma unroll
+        for (int e = 0; e < VEC; e++) st_from_float(&g[i][e], 0, 1.f);
+    auto load = [&](long long r) {
+        r = min(r, rows - 1);
+        nm = mean_in[r];
+        nr = rstd_in[r];
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int c = (i * group + lane) * VEC, at = FULL ? c : min(c, d - VEC);
+            nx[i].load(x + r * d + at);
+            ny[i].load(dy + r * d + at);
+        }
+    };
+    if (kAhead) load(row);
+#pragma unroll
+    for (int p = 0; p < P; p++) ag[p] = ab[p] = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; i++) {
         const int c = (i * group + lane) * VEC;
-#pragma unroll
-        for (int e = 0; e < VEC; e++) {
-            g[i][e] = 1.f;
-            ag[i][e] = ab[i][e] = 0.f;
-        }
-        if (gain && c < d) ld_w<W, VEC>(gain, c, g[i]);
+        if (FULL || (gain && c < d)) ld_w<W, VEC>(gain, c, g[i]);
     }
     const float inv_d = 1.f / d;
-    for (long long row = (long long)blockIdx.x * ng + gi; row < rows; row += (long long)gridDim.x * ng) {
-        const float mean = mean_in[row], rstd = rstd_in[row];
-        float h[NV][VEC], t[NV][VEC];
+    for (; row < rows; row += stride) {
+        if constexpr (kAhead && sizeof(W) == 2) {  // the weights stay packed: converted once they would take twice the registers
+            uint32_t* words = reinterpret_cast<uint32_t*>(g);
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const int c = (i * group + lane) * VEC;
-            if (c < d) {
-                ld_vec<T, VEC>(x + row * d + c, h[i]);
-                ld_vec<T, VEC>(dy + row * d + c, t[i]);
-            }
+            for (int i = 0; i < P; i++) asm volatile("" : "+r"(words[i]));
         }
-        float2 s = make_float2(0.f, 0.f);
+        if (!kAhead) load(row);
+        const float rstd = nr;
+        const float2 r2 = both(nr), m2 = both(-nm);
+        float2 h[P], t[P], sx = both(0.f), sy = both(0.f);
 #pragma unroll
         for (int i = 0; i < NV; i++)
-            if ((i * group + lane) * VEC < d) {
+            if (!FULL) ny[i].keep_if((i * group + lane) * VEC < d);  // so every sum stays as it is
 #pragma unroll
-                for (int e = 0; e < VEC; e++) {
-                    h[i][e] = (h[i][e] - mean) * rstd;
-                    ag[i][e] = fmaf(t[i][e], h[i][e], ag[i][e]);
-                    ab[i][e] += t[i][e];
-                    t[i][e] *= g[i][e];
-                    s.x += t[i][e];
-                    s.y = fmaf(t[i][e], h[i][e], s.y);
-                }
-            }
-        s = sum(s);
-        const float c0 = s.x * inv_d, c1 = s.y * inv_d;
+        for (int p = 0; p < P; p++) {
+            const int i = 2 * p / VEC, e = 2 * p % VEC, j = (2 * p + 1) / VEC, u = (2 * p + 1) % VEC;
+            h[p] = mul2(add2(make_float2(nx[i][e], nx[j][u]), m2), r2);
+            t[p] = make_float2(ny[i][e], ny[j][u]);
+            ag[p] = fma2(t[p], h[p], ag[p]);
+            ab[p] = add2(ab[p], t[p]);
+            if (FULL || gain) t[p] = mul2(t[p], make_float2(f_of(g[i][e]), f_of(g[j][u])));
+            sx = add2(sx, t[p]);
+            sy = fma2(t[p], h[p], sy);
+        }
+        if (kAhead) load(row + stride);
+        const float2 s = sum.two(sx.x + sx.y, sy.x + sy.y);
         if (dx) {
+            // rstd (t - c0 - h c1)
+            const float2 c0 = both(-s.x * inv_d * rstd), c1 = both(-s.y * inv_d * rstd);
+#pragma unroll
+            for (int p = 0; p < P; p++) t[p] = fma2(t[p], r2, fma2(h[p], c1, c0));
 #pragma unroll
             for (int i = 0; i < NV; i++) {
                 const int c = (i * group + lane) * VEC;
-                if (c >= d) continue;
-#pragma unroll
-                for (int e = 0; e < VEC; e++) t[i][e] = rstd * (t[i][e] - c0 - h[i][e] * c1);
-                st_vec<T, VEC>(dx + row * d + c, t[i]);
+                if (FULL || c < d) st_vec<T, VEC>(dx + row * d + c, reinterpret_cast<const float*>(t) + i * VEC);
             }
         }
     }
     if (!part) return;
     // the groups of the block add their columns one after the other
-    const int width = group * NV * VEC;
+    const int width = group * E;
+    const float *fg = reinterpret_cast<const float*>(ag), *fb = reinterpret_cast<const float*>(ab);
     for (int k = 0; k < ng; k++) {
         __syncthreads();
         if (gi == k) {
@@ -221,8 +329,8 @@ __global__ void __launch_bounds__(512) k_ln_backward(const T* __restrict__ dy, c
 #pragma unroll
                 for (int e = 0; e < VEC; e++) {
                     const int c = (i * group + lane) * VEC + e;
-                    cols[c] = k ? cols[c] + ag[i][e] : ag[i][e];
-                    cols[width + c] = k ? cols[width + c] + ab[i][e] : ab[i][e];
+                    cols[c] = k ? cols[c] + fg[i * VEC + e] : fg[i * VEC + e];
+                    cols[width + c] = k ? cols[width + c] + fb[i * VEC + e] : fb[i * VEC + e];
                 }
         }
     }
@@ -234,48 +342,43 @@ __global__ void __launch_bounds__(512) k_ln_backward(const T* __restrict__ dy, c
     }
 }
 
-// Adds the partial rows: a block takes 32 columns, its warps the partial rows
-// w, w + 8, ..., then the warps' sums in order.
-__global__ void __launch_bounds__(256) k_ln_columns(const float* __restrict__ part, int parts, int d,
-                                                   float* __restrict__ dgain, float* __restrict__ dbias) {
-    __shared__ float s[8][33];
+// Adds the partial rows: a block takes 32 columns, warp w the partial rows
+// w, w + 32, ... (all loads of a thread in flight), then the warps' sums in order.
+constexpr int kColWarps = 32;
+__global__ void __launch_bounds__(kColWarps * 32) k_ln_columns(const float* __restrict__ part, int parts, int d,
+                                                              float* __restrict__ dgain, float* __restrict__ dbias) {
+    __shared__ float s[kColWarps][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, n = 2 * d;
-    float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+    float t = 0.f;
     if (c < n) {
-        int p = w;
-        for (; p + 24 < parts; p += 32) {
-            a0 += part[(size_t)p * n + c];
-            a1 += part[(size_t)(p + 8) * n + c];
-            a2 += part[(size_t)(p + 16) * n + c];
-            a3 += part[(size_t)(p + 24) * n + c];
+        constexpr int kLoads = (kBwdBlocks + kColWarps - 1) / kColWarps;
+        float x[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; i++) {
+            const int p = w + i * kColWarps;
+            x[i] = p < parts ? part[(size_t)p * n + c] : 0.f;
         }
-        for (; p < parts; p += 8) a0 += part[(size_t)p * n + c];
+#pragma unroll
+        for (int i = 0; i < kLoads; i++) t += x[i];
     }
-    s[w][lane] = (a0 + a1) + (a2 + a3);
+    s[w][lane] = t;
     __syncthreads();
     if (w == 0 && c < n) {
-        float t = 0.f;
+        t = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; i++) t += s[i][lane];
+        for (int i = 0; i < kColWarps; i++) t += s[i][lane];
         float* out = c < d ? dgain : dbias;
         if (out) out[c < d ? c : c - d] = t;
     }
 }
 
-// The group of threads of a row: the smallest of 32, 64, ... 1,024 that
-// holds it, 0 if none does.
-int group_for(int d, int vec, int nv, int most) {
-    for (int t = 32; t <= most; t *= 2)
-        if ((long long)t * vec * nv >= d) return t;
-    return 0;
+// The group of threads of a row: the smallest of 32, 64, ... that holds it.
+int group_for(int d, int elems) {
+    int t = 32;
+    while (t * elems < d) t *= 2;
+    return t;
 }
-
-constexpr int kFwdVec = 4, kFwdScalar = 8;  // loads of a thread of the forward
-constexpr int kBwdElems = 16;               // elements of a thread of the backward
-constexpr int kFwdMost = 1024, kBwdMost = 512;
-// Blocks of the backward: two for each of the 148 SMs.
-constexpr int kBwdBlocks = 296;
 
 bool wide_rows(const LayerNormArgs& a) {
     const int V = a.dt == RET_F32 ? 4 : 8;
@@ -285,55 +388,54 @@ bool wide_rows(const LayerNormArgs& a) {
     return ok;
 }
 
-struct BwdPlan {
-    int group, threads, blocks;
-};
-BwdPlan bwd_plan(const LayerNormArgs& a, bool wide) {
-    BwdPlan p;
-    p.group = wide ? group_for(a.d, a.dt == RET_F32 ? 4 : 8, kBwdElems / (a.dt == RET_F32 ? 4 : 8), kBwdMost)
-                   : group_for(a.d, 1, kBwdElems, kBwdMost);
-    p.threads = std::max(256, p.group);
-    const long long ng = p.group ? p.threads / p.group : 1;
-    p.blocks = (int)std::min<long long>(kBwdBlocks, (a.rows + ng - 1) / ng);
-    return p;
+template <typename T, typename W, int VEC, int ELEMS>
+ret_status fwd_go(const LayerNormArgs& a, cudaStream_t s) {
+    const int group = group_for(a.d, ELEMS), threads = std::max(128, group), ng = threads / group;
+    const long long fit = kSms * (ELEMS > 16 ? 640 : 768) / threads;  // what the registers let an SM hold
+    const unsigned blocks = (unsigned)std::min<long long>(fit, (a.rows + ng - 1) / ng);
+    auto go = [&](auto kern) {
+        kern<<<blocks, threads, 0, s>>>((const T*)a.x, (const W*)a.gain, (const W*)a.bias, (T*)a.y, a.mean, a.rstd, a.rows,
+                                        a.d, (float)a.eps, group);
+        return check_launch("ret_layernorm_forward");
+    };
+    if constexpr (VEC > 1)
+        if (a.d == group * ELEMS && a.gain && a.bias) return go(k_ln_forward<T, W, VEC, ELEMS / VEC, true>);
+    return go(k_ln_forward<T, W, VEC, ELEMS / VEC, false>);
 }
-
 template <typename T, typename W>
 ret_status fwd(const LayerNormArgs& a, cudaStream_t s) {
     constexpr int V = 16 / (int)sizeof(T);
-    const bool wide = wide_rows(a);
-    int group = wide ? group_for(a.d, V, kFwdVec, kFwdMost) : group_for(a.d, 1, kFwdScalar, kFwdMost);
-    const int threads = std::max(128, group), ng = threads / group;
-    const long long blocks = (a.rows + ng - 1) / ng;
-    if (wide)
-        k_ln_forward<T, W, V, kFwdVec><<<(unsigned)blocks, threads, 0, s>>>(
-            (const T*)a.x, (const W*)a.gain, (const W*)a.bias, (T*)a.y, a.mean, a.rstd, a.rows, a.d, (float)a.eps, group);
-    else
-        k_ln_forward<T, W, 1, kFwdScalar><<<(unsigned)blocks, threads, 0, s>>>(
-            (const T*)a.x, (const W*)a.gain, (const W*)a.bias, (T*)a.y, a.mean, a.rstd, a.rows, a.d, (float)a.eps, group);
-    return check_launch("ret_layernorm_forward");
+    if (!wide_rows(a)) return fwd_go<T, W, 1, 16>(a, s);
+    // A lane takes 32 elements when a warp of 16 does not hold the row and there
+    // are rows for every group; few rows finish sooner with more threads each.
+    return a.d <= 512 || a.rows <= kSms ? fwd_go<T, W, V, 16>(a, s) : fwd_go<T, W, V, 32>(a, s);
 }
 
 template <typename T, typename W>
 ret_status bwd(const LayerNormArgs& a, cudaStream_t s) {
     constexpr int V = 16 / (int)sizeof(T);
-    const bool wide = wide_rows(a);
-    const BwdPlan p = bwd_plan(a, wide);
+    const int group = group_for(a.d, kBwdElems);
+    // Few large blocks when there are rows for all of them (fewer partial rows
+    // to write and add), small ones to spread few rows.
+    const bool many = a.rows >= (long long)kSms * (kBwdMost / group);
+    const int threads = many ? kBwdMost : std::max(128, group), ng = threads / group;
+    const int blocks = (int)std::min<long long>(many ? kSms : kBwdBlocks, (a.rows + ng - 1) / ng);
     float* part = a.dgain || a.dbias ? (float*)a.workspace : nullptr;
-    const int width = p.group * kBwdElems;
-    const size_t smem = part ? (size_t)2 * width * sizeof(float) : 0;  // at most 64 KB
+    const size_t smem = part ? (size_t)2 * group * kBwdElems * sizeof(float) : 0;  // at most 64 KB
     auto go = [&](auto kern) -> ret_status {
         if (smem > 48 * 1024) {
             cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (e != cudaSuccess) return fail(RET_ERR_CUDA, "ret_layernorm_backward: %s", cudaGetErrorString(e));
         }
-        kern<<<p.blocks, p.threads, smem, s>>>((const T*)a.dy, (const T*)a.x, a.mean, a.rstd, (const W*)a.gain, (T*)a.dx,
-                                               part, a.rows, a.d, p.group);
+        kern<<<blocks, threads, smem, s>>>((const T*)a.dy, (const T*)a.x, a.mean, a.rstd, (const W*)a.gain, (T*)a.dx, part,
+                                           a.rows, a.d, group);
         return check_launch("ret_layernorm_backward");
     };
-    ret_status st = wide ? go(k_ln_backward<T, W, V, kBwdElems / V>) : go(k_ln_backward<T, W, 1, kBwdElems>);
+    ret_status st = !wide_rows(a) ? go(k_ln_backward<T, W, 1, kBwdElems, false>)
+                    : a.d == group * kBwdElems && a.gain ? go(k_ln_backward<T, W, V, kBwdElems / V, true>)
+                                                         : go(k_ln_backward<T, W, V, kBwdElems / V, false>);
     if (st != RET_OK || !part) return st;
-    k_ln_columns<<<(2 * a.d + 31) / 32, 256, 0, s>>>(part, p.blocks, a.d, a.dgain, a.dbias);
+    k_ln_columns<<<(2 * a.d + 31) / 32, kColWarps * 32, 0, s>>>(part, blocks, a.d, a.dgain, a.dbias);
     return check_launch("ret_layernorm_backward: columns");
 }
 

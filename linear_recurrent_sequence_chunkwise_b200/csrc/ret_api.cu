@@ -1082,13 +1082,14 @@ ret_status ret_check_device_error(cudaStream_t stream) {
     t_err[0] = 0;
     cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return fail(RET_ERR_CUDA, "ret_check_device_error: %s", cudaGetErrorString(e));
-    int flag = 0, flag2 = 0, flag3 = 0, flag4 = 0;
+    int flag = 0, flag2 = 0, flag3 = 0, flag4 = 0, flag5 = 0;
     e = read_clear_error_chunk_ws(&flag);
     if (e == cudaSuccess) e = read_clear_error_gemm(&flag2);
     if (e == cudaSuccess) e = read_clear_error_delta(&flag3);
     if (e == cudaSuccess) e = read_clear_error_delta_grads(&flag4);
+    if (e == cudaSuccess) e = read_clear_error_delta_step(&flag5);
     if (e != cudaSuccess) return fail(RET_ERR_CUDA, "ret_check_device_error: %s", cudaGetErrorString(e));
-    flag |= flag2 | flag3 | flag4;
+    flag |= flag2 | flag3 | flag4 | flag5;
     if (flag) return fail(RET_ERR_TIMEOUT, "a kernel gave up a bounded wait (device error word %d)", flag);
     return RET_OK;
 }
