@@ -18,8 +18,8 @@
 // partial row, and a second kernel adds those in a fixed order (the result
 // does not depend on timing).  All sums are fp32.
 //
-// 8192 x 2048 bf16: forward %F%, backward %B% (with 8 elements in a lane and
-// eight warps a row: 28 and 39 us).
+// 8192 x 2048 bf16: forward 21 us, backward 22.5 + 3.7 us for the columns
+// (with 8 elements in a lane and eight warps a row: 28 and 39 us).
 #include <algorithm>
 
 #include "kernels.h"
@@ -39,7 +39,7 @@ __device__ __forceinline__ float f_of(__nv_bfloat16 x) { return __bfloat162float
 // VEC consecutive elements as they lie in memory; VEC * sizeof(T) is 16
 // (aligned) or VEC is 1.  A load behind the row's end reads the row's last
 // elements instead and is cleared where it is used: a branch around a load
-// would wait for the load (8,192 x 2,048 forward: %BR% with branches).
+// waits for the load where it ends.
 template <typename T, int VEC>
 struct alignas(VEC == 1 ? sizeof(T) : 16) Raw {
     T e[VEC];
@@ -55,18 +55,51 @@ struct alignas(VEC == 1 ? sizeof(T) : 16) Raw {
         if constexpr (VEC == 1) e[0] = p[0];
         else *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
     }
-    __device__ __forceinline__ float operator[](int i) const { return f_of(e[i]); }
 };
+// Elements 2 i and 2 i + 1 of an array in its own dtype.
+__device__ __forceinline__ float2 pair_of(const float* e, int i) { return make_float2(e[2 * i], e[2 * i + 1]); }
+__device__ __forceinline__ float2 pair_of(const __nv_bfloat16* e, int i) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(e)[i];
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ float2 pair_of(const Raw<T, VEC> (&r)[NV], int p) {
+    if constexpr (VEC == 1) return make_float2(f_of(r[2 * p].e[0]), f_of(r[2 * p + 1].e[0]));
+    else return pair_of(r[2 * p / VEC].e, p % (VEC / 2));
+}
+template <typename W, int VEC, int NV>
+__device__ __forceinline__ float2 pair_of(const W (&w)[NV][VEC], int p) {
+    if constexpr (VEC == 1) return make_float2(f_of(w[2 * p][0]), f_of(w[2 * p + 1][0]));
+    else return pair_of(w[2 * p / VEC], p % (VEC / 2));
+}
+// VEC elements from the pairs at f, rounded once.
 template <typename T, int VEC>
-__device__ __forceinline__ void st_vec(T* p, const float* f) {
-    if constexpr (VEC == 1) {
-        st_from_float(p, 0, f[0]);
+__device__ __forceinline__ void st_vec(T* p, const float2* f) {
+    static_assert(VEC > 1, "");
+    uint4 u;
+    if constexpr (sizeof(T) == 4) {
+        u = make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
     } else {
-        uint4 u;
-        T* e = reinterpret_cast<T*>(&u);
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < VEC; i++) st_from_float(e, i, f[i]);
-        *reinterpret_cast<uint4*>(p) = u;
+        for (int i = 0; i < 4; i++) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[i].x, f[i].y);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        u = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    *reinterpret_cast<uint4*>(p) = u;
+}
+// The row's elements from the thread's pairs.
+template <typename T, int VEC, int NV, bool FULL>
+__device__ __forceinline__ void st_row(T* p, const float2 (&f)[VEC * NV / 2], int d, int group, int lane) {
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        const int c = (i * group + lane) * VEC;
+        if (FULL || c < d) {
+            if constexpr (VEC == 1) st_from_float(p, c, i & 1 ? f[i / 2].y : f[i / 2].x);
+            else st_vec<T, VEC>(p + c, f + i * VEC / 2);
+        }
     }
 }
 // VEC weights at column c, in their own dtype (kept so in registers).
@@ -84,18 +117,20 @@ __device__ __forceinline__ void ld_w(const W* w, int c, W* f) {
 
 // Sums over the T threads of a group; every thread gets them.  `red`: words of
 // the group, alternating between two halves so that one barrier per sum is
-// enough.
+// enough.  `bar`: the group's named barrier, 0 for a group that is the block
+// (a block with a variable one holds 16 of an SM's 64 barriers: four blocks).
 struct GroupSum {
     float* red;  // [2][2 T / 32]
     int T, bar, half;
+    // For a group of a warp or of the whole block.
     __device__ __forceinline__ float one(float x) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (T == 32) return x;
         const int nw = T / 32;
         float* r = next(nw);
-        if ((threadIdx.x & 31) == 0) r[(threadIdx.x % T) >> 5] = x;
-        sync();
+        if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = x;
+        __syncthreads();
         x = r[0];
         for (int i = 1; i < nw; i++) x += r[i];
         return x;
@@ -151,6 +186,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // FULL: the group's loads cover the row exactly and both weights are given.
+// A group is a warp or the block.
 template <typename T, typename W, int VEC, int NV, bool FULL>
 __global__ void __launch_bounds__(512) k_ln_forward(const T* __restrict__ x, const W* __restrict__ gain,
                                                    const W* __restrict__ bias, T* __restrict__ y,
@@ -159,7 +195,7 @@ __global__ void __launch_bounds__(512) k_ln_forward(const T* __restrict__ x, con
     constexpr int P = VEC * NV / 2;
     __shared__ float red[64];
     const int gi = threadIdx.x / group, lane = threadIdx.x % group, ng = blockDim.x / group;
-    GroupSum sum{red + gi * 4 * (group / 32), group, 1 + gi, 0};
+    GroupSum sum{red, group, 0, 0};
     const float inv_d = 1.f / d;
     const long long stride = (long long)gridDim.x * ng;
     Raw<T, VEC> raw[NV];
@@ -171,17 +207,21 @@ __global__ void __launch_bounds__(512) k_ln_forward(const T* __restrict__ x, con
             raw[i].load(xr + (FULL ? c : min(c, d - VEC)));
         }
     };
+    // behind the row's end: zero
+    auto inside = [&](float2 f, int p) {
+        if (!FULL) {
+            if ((2 * p / VEC * group + lane) * VEC >= d) f.x = 0.f;
+            if (((2 * p + 1) / VEC * group + lane) * VEC >= d) f.y = 0.f;
+        }
+        return f;
+    };
     long long row = (long long)blockIdx.x * ng + gi;
     load(row);
     for (; row < rows; row += stride) {
         float2 f[P], s = both(0.f), v = s;
 #pragma unroll
         for (int p = 0; p < P; p++) {
-            f[p] = make_float2(raw[2 * p / VEC][2 * p % VEC], raw[(2 * p + 1) / VEC][(2 * p + 1) % VEC]);
-            if (!FULL) {
-                if ((2 * p / VEC * group + lane) * VEC >= d) f[p].x = 0.f;
-                if (((2 * p + 1) / VEC * group + lane) * VEC >= d) f[p].y = 0.f;
-            }
+            f[p] = inside(pair_of<T, VEC, NV>(raw, p), p);
             s = add2(s, f[p]);
         }
         load(row + stride);
@@ -189,11 +229,7 @@ __global__ void __launch_bounds__(512) k_ln_forward(const T* __restrict__ x, con
         const float2 m2 = both(-mean);
 #pragma unroll
         for (int p = 0; p < P; p++) {
-            f[p] = add2(f[p], m2);
-            if (!FULL) {  // behind the row's end: no distance
-                if ((2 * p / VEC * group + lane) * VEC >= d) f[p].x = 0.f;
-                if (((2 * p + 1) / VEC * group + lane) * VEC >= d) f[p].y = 0.f;
-            }
+            f[p] = inside(add2(f[p], m2), p);
             v = fma2(f[p], f[p], v);
         }
         const float rstd = 1.f / sqrtf(sum.one(v.x + v.y) * inv_d + eps);
@@ -202,34 +238,24 @@ __global__ void __launch_bounds__(512) k_ln_forward(const T* __restrict__ x, con
             if (rstd_out) rstd_out[row] = rstd;
         }
         const float2 r2 = both(rstd);
-#pragma unroll
-        for (int p = 0; p < P; p++) f[p] = mul2(f[p], r2);
+        alignas(16) W g[NV][VEC], b[NV][VEC];
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int c = (i * group + lane) * VEC, at = FULL ? c : min(c, d - VEC);
-            alignas(16) W g[VEC], b[VEC];
-            if (FULL || gain) ld_w<W, VEC>(gain, at, g);
-            if (FULL || bias) ld_w<W, VEC>(bias, at, b);
-            float t[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; e += 2) {
-                if (FULL && VEC > 1) {
-                    const float2 u = fma2(f[(i * VEC + e) / 2], make_float2(f_of(g[e]), f_of(g[(e + 1) % VEC])),
-                                          make_float2(f_of(b[e]), f_of(b[(e + 1) % VEC])));
-                    t[e] = u.x;
-                    t[(e + 1) % VEC] = u.y;
-                } else {
-#pragma unroll
-                    for (int k = e; k < VEC && k < e + 2; k++) {
-                        const int j = i * VEC + k;
-                        t[k] = j & 1 ? f[j / 2].y : f[j / 2].x;
-                        if (gain) t[k] *= f_of(g[k]);
-                        if (bias) t[k] += f_of(b[k]);
-                    }
-                }
-            }
-            if (FULL || c < d) st_vec<T, VEC>(y + row * d + c, t);
+            if (FULL || gain) ld_w<W, VEC>(gain, at, g[i]);
+            if (FULL || bias) ld_w<W, VEC>(bias, at, b[i]);
         }
+#pragma unroll
+        for (int p = 0; p < P; p++) {
+            f[p] = mul2(f[p], r2);
+            if (FULL) {
+                f[p] = fma2(f[p], pair_of<W, VEC, NV>(g, p), pair_of<W, VEC, NV>(b, p));
+            } else {
+                if (gain) f[p] = mul2(f[p], pair_of<W, VEC, NV>(g, p));
+                if (bias) f[p] = add2(f[p], pair_of<W, VEC, NV>(b, p));
+            }
+        }
+        st_row<T, VEC, NV, FULL>(y + row * d, f, d, group, lane);
     }
 }
 
@@ -243,7 +269,7 @@ __global__ void __launch_bounds__(kBwdMost) k_ln_backward(const T* __restrict__ 
                                                          int d, int group) {
     constexpr int E = VEC * NV, P = E / 2;
     // the next row's loads in flight, where they fit the registers
-    constexpr bool kAhead = FULL && sizeof(T) == 2;
+    constexpr bool kAhead = (FULL && sizeof(T) == 2) || E == 8;
     __shared__ __align__(8) float red[64];
     extern __shared__ float cols[];  // [2][group * E]: the block's column sums
     const int gi = threadIdx.x / group, lane = threadIdx.x % group, ng = blockDim.x / group;
@@ -260,7 +286,7 @@ __global__ void __launch_bounds__(kBwdMost) k_ln_backward(const T* __restrict__ 
 #pragma unroll
         for (int e = 0; e < VEC; e++) st_from_float(&g[i][e], 0, 1.f);
     auto load = [&](long long r) {
-        r = min(r, rows - 1);
+        if (r >= rows) return;
         nm = mean_in[r];
         nr = rstd_in[r];
 #pragma unroll
@@ -280,11 +306,6 @@ __global__ void __launch_bounds__(kBwdMost) k_ln_backward(const T* __restrict__ 
     }
     const float inv_d = 1.f / d;
     for (; row < rows; row += stride) {
-        if constexpr (kAhead && sizeof(W) == 2) {  // the weights stay packed: converted once they would take twice the registers
-            uint32_t* words = reinterpret_cast<uint32_t*>(g);
-#pragma unroll
-            for (int i = 0; i < P; i++) asm volatile("" : "+r"(words[i]));
-        }
         if (!kAhead) load(row);
         const float rstd = nr;
         const float2 r2 = both(nr), m2 = both(-nm);
@@ -294,12 +315,11 @@ __global__ void __launch_bounds__(kBwdMost) k_ln_backward(const T* __restrict__ 
             if (!FULL) ny[i].keep_if((i * group + lane) * VEC < d);  // so every sum stays as it is
 #pragma unroll
         for (int p = 0; p < P; p++) {
-            const int i = 2 * p / VEC, e = 2 * p % VEC, j = (2 * p + 1) / VEC, u = (2 * p + 1) % VEC;
-            h[p] = mul2(add2(make_float2(nx[i][e], nx[j][u]), m2), r2);
-            t[p] = make_float2(ny[i][e], ny[j][u]);
+            h[p] = mul2(add2(pair_of<T, VEC, NV>(nx, p), m2), r2);
+            t[p] = pair_of<T, VEC, NV>(ny, p);
             ag[p] = fma2(t[p], h[p], ag[p]);
             ab[p] = add2(ab[p], t[p]);
-            if (FULL || gain) t[p] = mul2(t[p], make_float2(f_of(g[i][e]), f_of(g[j][u])));
+            if (FULL || gain) t[p] = mul2(t[p], pair_of<W, VEC, NV>(g, p));
             sx = add2(sx, t[p]);
             sy = fma2(t[p], h[p], sy);
         }
@@ -310,11 +330,7 @@ __global__ void __launch_bounds__(kBwdMost) k_ln_backward(const T* __restrict__ 
             const float2 c0 = both(-s.x * inv_d * rstd), c1 = both(-s.y * inv_d * rstd);
 #pragma unroll
             for (int p = 0; p < P; p++) t[p] = fma2(t[p], r2, fma2(h[p], c1, c0));
-#pragma unroll
-            for (int i = 0; i < NV; i++) {
-                const int c = (i * group + lane) * VEC;
-                if (FULL || c < d) st_vec<T, VEC>(dx + row * d + c, reinterpret_cast<const float*>(t) + i * VEC);
-            }
+            st_row<T, VEC, NV, FULL>(dx + row * d, t, d, group, lane);
         }
     }
     if (!part) return;
@@ -390,7 +406,7 @@ bool wide_rows(const LayerNormArgs& a) {
 
 template <typename T, typename W, int VEC, int ELEMS>
 ret_status fwd_go(const LayerNormArgs& a, cudaStream_t s) {
-    const int group = group_for(a.d, ELEMS), threads = std::max(128, group), ng = threads / group;
+    const int group = group_for(a.d, ELEMS), threads = group == 32 ? 128 : group, ng = threads / group;
     const long long fit = kSms * (ELEMS > 16 ? 640 : 768) / threads;  // what the registers let an SM hold
     const unsigned blocks = (unsigned)std::min<long long>(fit, (a.rows + ng - 1) / ng);
     auto go = [&](auto kern) {
@@ -398,6 +414,7 @@ ret_status fwd_go(const LayerNormArgs& a, cudaStream_t s) {
                                         a.d, (float)a.eps, group);
         return check_launch("ret_layernorm_forward");
     };
+    if constexpr (ELEMS == 32) return go(k_ln_forward<T, W, VEC, ELEMS / VEC, true>);
     if constexpr (VEC > 1)
         if (a.d == group * ELEMS && a.gain && a.bias) return go(k_ln_forward<T, W, VEC, ELEMS / VEC, true>);
     return go(k_ln_forward<T, W, VEC, ELEMS / VEC, false>);
@@ -406,22 +423,27 @@ template <typename T, typename W>
 ret_status fwd(const LayerNormArgs& a, cudaStream_t s) {
     constexpr int V = 16 / (int)sizeof(T);
     if (!wide_rows(a)) return fwd_go<T, W, 1, 16>(a, s);
-    // A lane takes 32 elements when a warp of 16 does not hold the row and there
-    // are rows for every group; few rows finish sooner with more threads each.
-    return a.d <= 512 || a.rows <= kSms ? fwd_go<T, W, V, 16>(a, s) : fwd_go<T, W, V, 32>(a, s);
+    // A lane takes 32 bf16 elements when two warps of them hold the row exactly
+    // and there are rows for every group; few rows finish sooner with more
+    // threads each, and 32 in fp32 do not fit the registers.
+    if constexpr (V == 8)
+        if (a.rows > kSms && a.d > 512 && a.gain && a.bias && a.d == group_for(a.d, 32) * 32) return fwd_go<T, W, V, 32>(a, s);
+    return fwd_go<T, W, V, 16>(a, s);
 }
 
 template <typename T, typename W>
 ret_status bwd(const LayerNormArgs& a, cudaStream_t s) {
     constexpr int V = 16 / (int)sizeof(T);
-    const int group = group_for(a.d, kBwdElems);
+    // element by element eight in a thread leave room for the next row's loads
+    const bool wide = wide_rows(a);
+    const int elems = wide || a.d > 8 * kBwdMost ? kBwdElems : 8, group = group_for(a.d, elems);
     // Few large blocks when there are rows for all of them (fewer partial rows
     // to write and add), small ones to spread few rows.
     const bool many = a.rows >= (long long)kSms * (kBwdMost / group);
     const int threads = many ? kBwdMost : std::max(128, group), ng = threads / group;
     const int blocks = (int)std::min<long long>(many ? kSms : kBwdBlocks, (a.rows + ng - 1) / ng);
     float* part = a.dgain || a.dbias ? (float*)a.workspace : nullptr;
-    const size_t smem = part ? (size_t)2 * group * kBwdElems * sizeof(float) : 0;  // at most 64 KB
+    const size_t smem = part ? (size_t)2 * group * elems * sizeof(float) : 0;  // at most 64 KB
     auto go = [&](auto kern) -> ret_status {
         if (smem > 48 * 1024) {
             cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -431,7 +453,7 @@ ret_status bwd(const LayerNormArgs& a, cudaStream_t s) {
                                            a.rows, a.d, group);
         return check_launch("ret_layernorm_backward");
     };
-    ret_status st = !wide_rows(a) ? go(k_ln_backward<T, W, 1, kBwdElems, false>)
+    ret_status st = !wide ? (elems == 8 ? go(k_ln_backward<T, W, 1, 8, false>) : go(k_ln_backward<T, W, 1, kBwdElems, false>))
                     : a.d == group * kBwdElems && a.gain ? go(k_ln_backward<T, W, V, kBwdElems / V, true>)
                                                          : go(k_ln_backward<T, W, V, kBwdElems / V, false>);
     if (st != RET_OK || !part) return st;
