@@ -1,6 +1,5 @@
 // delta_util.cuh -- what the chunked kernels of the gated delta rule share:
-// the chunk's formulas, the workspace tiles, warp-level matrix products and
-// the split of an fp32 value into two bf16 terms.
+// the chunk's formulas, the number format, the workspace, warp-level products.
 //
 // Within a chunk of C = 64 tokens, with G_i the sum of g up to token i,
 // D_ij = exp(G_i - G_j) for i >= j, M_ij = D_ij (k_i . k_j) for i > j:
@@ -11,12 +10,20 @@
 //     S1 = exp(G_C) S0 + K^T diag(exp(G_C - G)) U.
 // Every exponent is a sum of g over tokens of the chunk, so never positive.
 //
-// Precision.  q, k, v are bf16, everything computed from them is held in fp32
-// and enters a matrix product as hi + lo, two bf16 terms whose sum is within
-// 2^-17 of the value: x y is hi hi + hi lo + lo hi (one product less where a
-// factor is an input, exact in bf16).  One bf16 term would leave the carried
-// state 2^-9 off after every chunk.
+// Numbers.  The tensor cores multiply fp16.  What is computed (S, R, U, T, P and
+// the gradients) is held in fp32 and enters a product as two fp16 terms, hi + lo,
+// 22 bits: x y = hi hi + hi lo + lo hi (two bf16 terms carry 16 bits, which the
+// gradients of the gates, differences of sums, do not survive).  fp16 has a
+// narrow range, so everything is brought near one by powers of two, which are
+// exact:
+//   * a key k_i = s_i k'_i with |k'_i| in [1, 2) (a query likewise); the rule for
+//     k' has beta' = beta s^2, v' = v / s, u' = s u, and the same S and G;
+//   * S, R, U (S', Y, U of the gradients) are scaled by the largest value of a
+//     warp's part, and the products of parts are joined in fp32.
+// A bf16 output takes one fp16 term of S, U and P (2^-12, against its own 2^-8).
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -27,29 +34,61 @@ namespace ret {
 namespace delta {
 
 constexpr int C = 64;              // tokens of a chunk
-constexpr int kTile = C * C * 2;   // bytes of a 64 x 64 bf16 tile (128-byte rows, swizzled)
-constexpr int kSlice = 64;         // value columns of a tile
-constexpr int kGates = 3 * C * 4;       // bytes: exp(G), exp(G_C - G), beta in fp32
-constexpr int kGateRow = kGates + C * 8;  // and G in 64 bits
+constexpr int kTile = C * C * 2;   // bytes of a 64 x 64 fp16 tile (128-byte rows, swizzled)
+// Gates of a chunk, 64 values each: in fp32 exp(G), exp(G_C - G), beta', 1 / s
+// of the keys, s of the queries; then G in 64 bits.
+constexpr int gEG = 0, gEC = C, gBeta = 2 * C, gIk = 3 * C, gSq = 4 * C;
+constexpr int kGates = 5 * C * 4;
+constexpr int kGateRow = kGates + C * 8;
 // Below this a decay is zero in fp32; keeps -inf out of the sums.
 constexpr float kMinG = -128.f;
 
 inline int chunks_of(int N) { return (N + C - 1) / C; }
-inline int slices_of(int dv) { return (dv + kSlice - 1) / kSlice; }
 
 __device__ __forceinline__ int length_of(const int* lengths, int b, int N) {
     return lengths ? max(0, min(lengths[b], N)) : N;
 }
 
+// The workspace.  Per (sequence, key head, chunk): K', Q' [dk/64][64][128 B].
+// Per (sequence, head, chunk): T hi, T lo, P hi, P lo; the gates.
+struct Tables {
+    uint8_t *keys, *tiles, *gates;
+};
+inline size_t table_bytes(const DeltaArgs& a) {
+    const size_t nc = chunks_of(a.N);
+    return a.B * nc * ((size_t)a.H * (4 * kTile + kGateRow) + (size_t)a.Hk * 4 * C * a.dk);
+}
+inline Tables tables_at(const DeltaArgs& a, void* ws) {
+    const size_t nc = chunks_of(a.N);
+    Tables t;
+    t.keys = reinterpret_cast<uint8_t*>(ws);
+    t.tiles = t.keys + a.B * nc * a.Hk * 4 * C * a.dk;
+    t.gates = t.tiles + a.B * nc * a.H * 4 * kTile;
+    return t;
+}
+
 // ------------------------------------------------------- warp-level products
 
-// D[16 x 8] += A[16 x 16] B[16 x 8], bf16 in, fp32 accumulate.
+// D[16 x 8] += A[16 x 16] B[16 x 8], fp16 in, fp32 accumulate.
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
         "%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The same with D[16 x 8] = A B.
+__device__ __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, "
+        "%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void add_scaled(float (&d)[4], const float (&x)[4], float s) {
+#pragma unroll
+    for (int e = 0; e < 4; e++) d[e] = fmaf(s, x[e], d[e]);
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -69,43 +108,76 @@ __device__ __forceinline__ void stsm4_t(uint32_t addr, const uint32_t (&r)[4]) {
                  "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
 }
-
-// Address of 16-byte piece `c` (8 bf16) of row `r` of a tile of 64-row slabs
-// with 128-byte swizzled rows.
-__device__ __forceinline__ uint32_t tile_at(uint32_t base, int r, int c) {
-    return base + (uint32_t)(c >> 3) * 8192u + (uint32_t)r * 128u + (uint32_t)(((c ^ r) & 7) << 4);
+// Transpose of an 8 x 8 matrix of 16-bit values held across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
 }
 
+// Offset of 16-byte piece `c` (8 values) of row `r` in slabs of ROWS rows of
+// 128 swizzled bytes.
+template <int ROWS = C>
+__device__ __forceinline__ uint32_t tile_at(int r, int c) {
+    return (uint32_t)(c >> 3) * (ROWS * 128u) + (uint32_t)r * 128u + (uint32_t)(((c ^ r) & 7) << 4);
+}
 // The four 8 x 8 blocks of a 16-row, 16-column part at (row, piece):
-// rows first (blocks 0, 1 side by side): a B operand whose rows are n.
+// rows first (blocks 0, 1 side by side): a B operand whose rows are n, or,
+// transposed, an A operand whose rows are k.
+template <int ROWS = C>
 __device__ __forceinline__ uint32_t at_n(uint32_t base, int row, int piece, int lane) {
     const int m = lane >> 3;
-    return tile_at(base, row + ((m >> 1) << 3) + (lane & 7), piece + (m & 1));
+    return base + tile_at<ROWS>(row + ((m >> 1) << 3) + (lane & 7), piece + (m & 1));
 }
-// columns first (blocks 0, 1 on top of each other): an A operand, or
-// (transposed) a B operand whose rows are k.
+// columns first (blocks 0, 1 on top of each other): an A operand whose rows
+// are m, or, transposed, a B operand whose rows are k.
+template <int ROWS = C>
 __device__ __forceinline__ uint32_t at_k(uint32_t base, int row, int piece, int lane) {
     const int m = lane >> 3;
-    return tile_at(base, row + ((m & 1) << 3) + (lane & 7), piece + (m >> 1));
+    return base + tile_at<ROWS>(row + ((m & 1) << 3) + (lane & 7), piece + (m >> 1));
 }
 
-// x = hi + lo in bf16 pairs.
+__device__ __forceinline__ uint32_t pack_h2(float x0, float x1) {
+    const __half2 h = __floats2half2_rn(x0, x1);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_h2(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
+
+// x = hi + lo, pairs of fp16.
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-    hi = tc::pack_bf16x2(x0, x1);
-    lo = tc::pack_bf16x2(x0 - tc::bf16lo(hi), x1 - tc::bf16hi(hi));
+    hi = pack_h2(x0, x1);
+    const float2 h = unpack_h2(hi);
+    lo = pack_h2(x0 - h.x, x1 - h.y);
 }
-// The A operand (16 x 16) from two neighbouring accumulator tiles.
-__device__ __forceinline__ void split_a(const float (&x)[4], const float (&y)[4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-    split2(x[0], x[1], hi[0], lo[0]);
-    split2(x[2], x[3], hi[1], lo[1]);
-    split2(y[0], y[1], hi[2], lo[2]);
-    split2(y[2], y[3], hi[3], lo[3]);
+// The A operand (16 x 16) from two neighbouring accumulator tiles, scaled by s.
+__device__ __forceinline__ void split_a(const float (&x)[4], const float (&y)[4], float s, uint32_t (&hi)[4],
+                                        uint32_t (&lo)[4]) {
+    split2(x[0] * s, x[1] * s, hi[0], lo[0]);
+    split2(x[2] * s, x[3] * s, hi[1], lo[1]);
+    split2(y[0] * s, y[1] * s, hi[2], lo[2]);
+    split2(y[2] * s, y[3] * s, hi[3], lo[3]);
 }
-__device__ __forceinline__ void round_a(const float (&x)[4], const float (&y)[4], uint32_t (&hi)[4]) {
-    hi[0] = tc::pack_bf16x2(x[0], x[1]);
-    hi[1] = tc::pack_bf16x2(x[2], x[3]);
-    hi[2] = tc::pack_bf16x2(y[0], y[1]);
-    hi[3] = tc::pack_bf16x2(y[2], y[3]);
+
+// The power of two that brings a largest value m >= 0 into [4, 8), and its
+// inverse.  (Headroom to fp16's 65,504: sums of 64 terms and the solve.)
+__device__ __forceinline__ float scale_for(float m, float& inverse) {
+    const int e = (__float_as_int(m) >> 23) & 255;
+    const int s = e == 0 || e == 255 ? 127 : min(max(256 - e, 27), 227);
+    inverse = __int_as_float((254 - s) << 23);
+    return __int_as_float(s << 23);
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+// The scale of a warp's values (a pair of accumulator tiles).
+__device__ __forceinline__ float scale_of(const float (&x)[4], const float (&y)[4], float& inverse) {
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; e++) m = fmaxf(m, fmaxf(fabsf(x[e]), fabsf(y[e])));
+    return scale_for(warp_max(m), inverse);
 }
 
 // Untiled asynchronous copy of `bytes` (a multiple of 16) into shared memory.
@@ -116,34 +188,26 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
-// Clears rows L .. 63 of a tile of `pieces` 16-byte pieces a row (a warp's work).
-__device__ __forceinline__ void clear_rows(uint8_t* tile, int L, int pieces, int lane) {
-    for (int i = lane; i < (C - L) * pieces; i += 32)
-        *reinterpret_cast<uint4*>(tile + tile_at(0, L + i / pieces, i % pieces)) = make_uint4(0, 0, 0, 0);
-}
+// The chunk tables (k_delta_prep.cu).
+ret_status launch_prep(const DeltaArgs& a, const Tables& t, cudaStream_t s);
 
-// [B, N, heads, d] bf16 as a {d, heads, N, B} tensor, boxes of one head's
-// chunk, 64 columns wide.
-inline bool chunk_map(CUtensorMap* m, const void* p, int B, int N, int heads, int d) {
-    const uint64_t dims[4] = {(uint64_t)d, (uint64_t)heads, (uint64_t)N, (uint64_t)B};
-    const uint64_t strides[3] = {(uint64_t)d * 2, (uint64_t)heads * d * 2, (uint64_t)N * heads * d * 2};
-    const uint32_t box[4] = {64, 1, (uint32_t)C, 1};
-    return make_tmap_bf16(m, p, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-// The chunk tables (k_delta_chunk.cu): T, P and the gates of every chunk.
-ret_status launch_prep(const DeltaArgs& a, uint8_t* tiles, uint8_t* gates, cudaStream_t s);
-
-// The backward's two chains (k_delta_chunk.cu).  Per (chunk, slice of 64 value
-// columns), transposed (a row per value column), hi then lo:
-//   s   [dk/64][64][128 B]  the state before the chunk
-//   u   [64][128 B]         the corrections
-//   ds  [dk/64][64][128 B]  the gradient of the state after the chunk
-//   y   [64][128 B]         dY = T^T dU
-struct Kept {
-    uint8_t *s, *u, *ds, *y;
+// What the backward's two chains (k_delta_chunk.cu) keep, one record per
+// (chunk, group of 16 value columns); the values transposed (a row per value
+// column), hi then lo:
+//   s   [hi, lo][dk/64][16][64]  the state before the chunk
+//   ds  the same                 the gradient of the state after it
+//   u   [hi, lo][16][64]         the corrections U'
+//   y   the same                 dY = T^T dU
+//   o   [16][64]                 dO' = s_q dO, one term
+//   f   5 fp32: the inverse scales of s, ds, u, y, o
+template <int DK>
+struct Record {
+    static constexpr int s = 0, ds = 64 * DK, u = 128 * DK, y = u + 4096, o = y + 4096, f = o + 2048, bytes = f + 128;
 };
-ret_status launch_chains(const DeltaArgs& a, const uint8_t* tiles, const uint8_t* gates, const Kept& kept, cudaStream_t s);
+inline size_t record_bytes(int dk) { return 128 * (size_t)dk + 4096 * 2 + 2048 + 128; }
+enum : int { fS = 0, fDs = 1, fU = 2, fY = 3, fO = 4 };
+__host__ __device__ __forceinline__ int groups_of(int dv) { return (dv + 15) / 16; }
+ret_status launch_chains(const DeltaArgs& a, const Tables& t, uint8_t* records, cudaStream_t s);
 
 }  // namespace delta
 }  // namespace ret
