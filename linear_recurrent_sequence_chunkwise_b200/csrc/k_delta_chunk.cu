@@ -193,15 +193,18 @@ __device__ __forceinline__ void write_state(const float (&S)[N][4], float* p, in
 }
 
 // [16 x 16] bf16 (16 tokens, 16 columns) of a [B, N, H, dv] tensor, a 16-byte
-// piece a lane; zeros behind the sequence's end and behind dv.  The address is
-// clamped, so no branch is around the load.
+// piece a lane.  A chunk ahead the address is clamped and nothing looks at the
+// value (a branch or a select there would wait for the load); where it is used,
+// what lies behind the sequence's end and behind dv becomes zero.
 struct Rows {
     const __nv_bfloat16* p;  // of the (sequence, head), at this lane's columns
     size_t pitch;
     int len;
     bool cols;
-    __device__ __forceinline__ uint4 operator()(int token) const {
-        uint4 x = *reinterpret_cast<const uint4*>(p + (size_t)min(token, len - 1) * pitch);
+    __device__ __forceinline__ uint4 load(int token) const {
+        return *reinterpret_cast<const uint4*>(p + (size_t)min(token, len - 1) * pitch);
+    }
+    __device__ __forceinline__ uint4 use(uint4 x, int token) const {
         if (token >= len || !cols) x = make_uint4(0, 0, 0, 0);
         return x;
     }
@@ -251,15 +254,16 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
         uint4 vn[4];
         if (n_chunks)
 #pragma unroll
-            for (int i = 0; i < 4; i++) vn[i] = vrows(16 * i + (lane >> 1));
+            for (int i = 0; i < 4; i++) vn[i] = vrows.load(16 * i + (lane >> 1));
         for (int c = 0; c < n_chunks; c++) {
             uint8_t* st = sh.sm + (c % NS) * Pl::stage;
             const uint32_t sK = tc::smem_u32(st), sT = sK + Pl::oT;
             const float* gt = reinterpret_cast<const float*>(st + Pl::oGate);
 #pragma unroll
-            for (int i = 0; i < 4; i++) *reinterpret_cast<uint4*>(slot + 512 * i + 16 * lane) = vn[i];
+            for (int i = 0; i < 4; i++)
+                *reinterpret_cast<uint4*>(slot + 512 * i + 16 * lane) = vrows.use(vn[i], c * C + 16 * i + (lane >> 1));
 #pragma unroll
-            for (int i = 0; i < 4; i++) vn[i] = vrows((c + 1) * C + 16 * i + (lane >> 1));
+            for (int i = 0; i < 4; i++) vn[i] = vrows.load((c + 1) * C + 16 * i + (lane >> 1));
 
             // X^T = S^T K^T; the helper gets the operand tiles
             float inv;
@@ -275,15 +279,11 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                 split_a(S[2 * kk], S[2 * kk + 1], ss, hi, lo);
                 put4(sf + kk * 512, hi, lane);
                 if constexpr (Pl::terms == 2) put4(sf + Pl::sHalf + kk * 512, lo, lane);
+                uint32_t bk[4][4];
 #pragma unroll
-                for (int p = 0; p < 4; p++) {
-                    uint32_t bk[4];
-                    ldsm4(bk, at_n(sK, 16 * p, 2 * kk, lane));
-                    mma(X[2 * p], hi, bk[0], bk[1]);
-                    mma(X[2 * p + 1], hi, bk[2], bk[3]);
-                    mma(X[2 * p], lo, bk[0], bk[1]);
-                    mma(X[2 * p + 1], lo, bk[2], bk[3]);
-                }
+                for (int p = 0; p < 4; p++) ldsm4(bk[p], at_n(sK, 16 * p, 2 * kk, lane));
+                mma_row<0, 4>(X, hi, bk);
+                mma_row<0, 4>(X, lo, bk);
             }
             if (lane == 0) sh.s_inv[cg] = si;
             signal(sh.s_ready + cg, lane);
@@ -317,18 +317,20 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
             for (int j = 0; j < 4; j++) {
                 uint32_t rh[4], rl[4];
                 split_a(X[2 * j], X[2 * j + 1], rs, rh, rl);
+                uint32_t th[4][4], tl[4][4];
 #pragma unroll
                 for (int p = j; p < 4; p++) {
-                    uint32_t th[4], tl[4];
-                    ldsm4(th, at_n(sT, 16 * p, 2 * j, lane));
-                    ldsm4(tl, at_n(sT + kTile, 16 * p, 2 * j, lane));
-                    mma(U[2 * p], rh, th[0], th[1]);
-                    mma(U[2 * p + 1], rh, th[2], th[3]);
-                    mma(U[2 * p], rl, th[0], th[1]);
-                    mma(U[2 * p + 1], rl, th[2], th[3]);
-                    mma(U[2 * p], rh, tl[0], tl[1]);
-                    mma(U[2 * p + 1], rh, tl[2], tl[3]);
+                    ldsm4(th[p], at_n(sT, 16 * p, 2 * j, lane));
+                    ldsm4(tl[p], at_n(sT + kTile, 16 * p, 2 * j, lane));
                 }
+#pragma unroll
+                for (int k = 0; k < 3; k++)
+#pragma unroll
+                    for (int p = j; p < 4; p++) {
+                        const uint32_t(&b)[4] = k == 2 ? tl[p] : th[p];
+                        mma(U[2 * p], k == 1 ? rl : rh, b[0], b[1]);
+                        mma(U[2 * p + 1], k == 1 ? rl : rh, b[2], b[3]);
+                    }
             }
             float ui = 0.f;
             const float us = tiles_scale(U, ui);  // of ri-scaled values: U is still times rs
@@ -351,31 +353,26 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
 #pragma unroll
             for (int j = 0; j < 4; j++) split_a(U[2 * j], U[2 * j + 1], 1.f, uh[j], ul[j]);
 #pragma unroll
-            for (int d = 0; d < KK; d += 2) {
-                float acc[4][4];
+            for (int d = 0; d < KK; d += 4) {
+                float acc[8][4];
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    uint32_t b0[4], b1[4];
-                    ldsm4_t(b0, at_k(sK, 16 * j, 2 * d, lane));
-                    ldsm4_t(b1, at_k(sK, 16 * j, 2 * d + 2, lane));
+                    uint32_t b[4][4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) ldsm4_t(b[i], at_k(sK, 16 * j, 2 * (d + i), lane));
                     if (j == 0) {
-                        mma0(acc[0], uh[j], b0[0], b0[1]);
-                        mma0(acc[1], uh[j], b0[2], b0[3]);
-                        mma0(acc[2], uh[j], b1[0], b1[1]);
-                        mma0(acc[3], uh[j], b1[2], b1[3]);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            mma0(acc[2 * i], uh[j], b[i][0], b[i][1]);
+                            mma0(acc[2 * i + 1], uh[j], b[i][2], b[i][3]);
+                        }
                     } else {
-                        mma(acc[0], uh[j], b0[0], b0[1]);
-                        mma(acc[1], uh[j], b0[2], b0[3]);
-                        mma(acc[2], uh[j], b1[0], b1[1]);
-                        mma(acc[3], uh[j], b1[2], b1[3]);
+                        mma_row<0, 4>(acc, uh[j], b);
                     }
-                    mma(acc[0], ul[j], b0[0], b0[1]);
-                    mma(acc[1], ul[j], b0[2], b0[3]);
-                    mma(acc[2], ul[j], b1[0], b1[1]);
-                    mma(acc[3], ul[j], b1[2], b1[3]);
+                    mma_row<0, 4>(acc, ul[j], b);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; i++)
+                for (int i = 0; i < 8; i++)
 #pragma unroll
                     for (int e = 0; e < 4; e++) S[2 * d + i][e] = fmaf(ui, acc[i][e], eC * S[2 * d + i][e]);
             }
@@ -441,17 +438,11 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                 uint32_t hi[4], lo[4];
                 get4(sf + kk * 512, hi, lane);
                 if constexpr (Pl::terms == 2) get4(sf + Pl::sHalf + kk * 512, lo, lane);
+                uint32_t bq[4][4];
 #pragma unroll
-                for (int p = 0; p < 4; p++) {
-                    uint32_t bq[4];
-                    ldsm4(bq, at_n(sQ, 16 * p, 2 * kk, lane));
-                    mma(O[2 * p], hi, bq[0], bq[1]);
-                    mma(O[2 * p + 1], hi, bq[2], bq[3]);
-                    if constexpr (Pl::terms == 2) {
-                        mma(O[2 * p], lo, bq[0], bq[1]);
-                        mma(O[2 * p + 1], lo, bq[2], bq[3]);
-                    }
-                }
+                for (int p = 0; p < 4; p++) ldsm4(bq[p], at_n(sQ, 16 * p, 2 * kk, lane));
+                mma_row<0, 4>(O, hi, bq);
+                if constexpr (Pl::terms == 2) mma_row<0, 4>(O, lo, bq);
             }
             const float si = sh.s_inv[cg];
             signal(sh.s_free + cg, lane);
@@ -572,15 +563,11 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
                 split_a(S[2 * kk], S[2 * kk + 1], ss, hi, lo);
                 put4(sf + kk * 512, hi, lane);
                 put4(sf + Pl::sHalf + kk * 512, lo, lane);
+                uint32_t bk[4][4];
 #pragma unroll
-                for (int p = 0; p < 4; p++) {
-                    uint32_t bk[4];
-                    ldsm4(bk, at_n(sK, 16 * p, 2 * kk, lane));
-                    mma(U[2 * p], hi, bk[0], bk[1]);
-                    mma(U[2 * p + 1], hi, bk[2], bk[3]);
-                    mma(U[2 * p], lo, bk[0], bk[1]);
-                    mma(U[2 * p + 1], lo, bk[2], bk[3]);
-                }
+                for (int p = 0; p < 4; p++) ldsm4(bk[p], at_n(sK, 16 * p, 2 * kk, lane));
+                mma_row<0, 4>(U, hi, bk);
+                mma_row<0, 4>(U, lo, bk);
             }
             if (lane == 0) sh.s_inv[cg] = si;
             signal(sh.s_ready + cg, lane);
@@ -601,18 +588,20 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
             for (int i = 0; i < 4; i++) {
                 uint32_t uh[4], ul[4];
                 split_a(U[2 * i], U[2 * i + 1], us, uh, ul);
+                uint32_t th[4][4], tl[4][4];
 #pragma unroll
                 for (int d = 0; d <= i; d++) {
-                    uint32_t th[4], tl[4];
-                    ldsm4_t(th, at_k(sT, 16 * i, 2 * d, lane));
-                    ldsm4_t(tl, at_k(sT + kTile, 16 * i, 2 * d, lane));
-                    mma(Y[2 * d], uh, th[0], th[1]);
-                    mma(Y[2 * d + 1], uh, th[2], th[3]);
-                    mma(Y[2 * d], ul, th[0], th[1]);
-                    mma(Y[2 * d + 1], ul, th[2], th[3]);
-                    mma(Y[2 * d], uh, tl[0], tl[1]);
-                    mma(Y[2 * d + 1], uh, tl[2], tl[3]);
+                    ldsm4_t(th[d], at_k(sT, 16 * i, 2 * d, lane));
+                    ldsm4_t(tl[d], at_k(sT + kTile, 16 * i, 2 * d, lane));
                 }
+#pragma unroll
+                for (int k = 0; k < 3; k++)
+#pragma unroll
+                    for (int d = 0; d <= i; d++) {
+                        const uint32_t(&b)[4] = k == 2 ? tl[d] : th[d];
+                        mma(Y[2 * d], k == 1 ? ul : uh, b[0], b[1]);
+                        mma(Y[2 * d + 1], k == 1 ? ul : uh, b[2], b[3]);
+                    }
             }
             const float ys = tiles_scale(Y, inv);  // of us-scaled values
             const float yi = inv * ui;
@@ -634,31 +623,26 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
 #pragma unroll
             for (int j = 0; j < 4; j++) split_a(Y[2 * j], Y[2 * j + 1], 1.f, yh[j], yl[j]);
 #pragma unroll
-            for (int d = 0; d < KK; d += 2) {
-                float acc[4][4];
+            for (int d = 0; d < KK; d += 4) {
+                float acc[8][4];
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    uint32_t b0[4], b1[4];
-                    ldsm4_t(b0, at_k(sK, 16 * j, 2 * d, lane));
-                    ldsm4_t(b1, at_k(sK, 16 * j, 2 * d + 2, lane));
+                    uint32_t b[4][4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) ldsm4_t(b[i], at_k(sK, 16 * j, 2 * (d + i), lane));
                     if (j == 0) {
-                        mma0(acc[0], yh[j], b0[0], b0[1]);
-                        mma0(acc[1], yh[j], b0[2], b0[3]);
-                        mma0(acc[2], yh[j], b1[0], b1[1]);
-                        mma0(acc[3], yh[j], b1[2], b1[3]);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            mma0(acc[2 * i], yh[j], b[i][0], b[i][1]);
+                            mma0(acc[2 * i + 1], yh[j], b[i][2], b[i][3]);
+                        }
                     } else {
-                        mma(acc[0], yh[j], b0[0], b0[1]);
-                        mma(acc[1], yh[j], b0[2], b0[3]);
-                        mma(acc[2], yh[j], b1[0], b1[1]);
-                        mma(acc[3], yh[j], b1[2], b1[3]);
+                        mma_row<0, 4>(acc, yh[j], b);
                     }
-                    mma(acc[0], yl[j], b0[0], b0[1]);
-                    mma(acc[1], yl[j], b0[2], b0[3]);
-                    mma(acc[2], yl[j], b1[0], b1[1]);
-                    mma(acc[3], yl[j], b1[2], b1[3]);
+                    mma_row<0, 4>(acc, yl[j], b);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
+                for (int i = 0; i < 8; i++) {
                     const float4 z = zf[32 * (2 * d + i)];
                     S[2 * d + i][0] = fmaf(yi, acc[i][0], fmaf(eC, S[2 * d + i][0], z.x));
                     S[2 * d + i][1] = fmaf(yi, acc[i][1], fmaf(eC, S[2 * d + i][1], z.y));
@@ -686,7 +670,7 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
     uint4 on[4];
     if (n_chunks)
 #pragma unroll
-        for (int i = 0; i < 4; i++) on[i] = orows((n_chunks - 1) * C + 16 * i + (lane >> 1));
+        for (int i = 0; i < 4; i++) on[i] = orows.load((n_chunks - 1) * C + 16 * i + (lane >> 1));
     for (int it = 0; it < n_chunks; it++) {
         if (feeds && it + NS - 1 < n_chunks) load(it + NS - 1);
         __syncwarp();
@@ -702,7 +686,7 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
 #pragma unroll
             for (int p = 0; p < 4; p++) {
                 uint32_t v4[4];
-                transpose16(slot + 512 * p, on[p], lane, v4);
+                transpose16(slot + 512 * p, orows.use(on[p], c * C + 16 * p + (lane >> 1)), lane, v4);
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
                     o[2 * p + i][0] = tc::bf16lo(v4[2 * i]);
@@ -713,7 +697,7 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
             }
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; i++) on[i] = orows(max(c - 1, 0) * C + 16 * i + (lane >> 1));
+            for (int i = 0; i < 4; i++) on[i] = orows.load(max(c - 1, 0) * C + 16 * i + (lane >> 1));
             scale_tokens(o, gt + gSq, 1.f, t);
             float oi;
             const float os = tiles_scale(o, oi);
@@ -730,15 +714,14 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
 #pragma unroll
             for (int i = 0; i < 4; i++)
 #pragma unroll
-                for (int d = 0; d <= i; d++) {
-                    uint32_t ph[4], pl[4];
-                    ldsm4_t(ph, at_k(sP, 16 * i, 2 * d, lane));
-                    ldsm4_t(pl, at_k(sP + kTile, 16 * i, 2 * d, lane));
-                    mma(U[2 * d], oh[i], ph[0], ph[1]);
-                    mma(U[2 * d + 1], oh[i], ph[2], ph[3]);
-                    mma(U[2 * d], oh[i], pl[0], pl[1]);
-                    mma(U[2 * d + 1], oh[i], pl[2], pl[3]);
-                }
+                for (int k = 0; k < 2; k++)
+#pragma unroll
+                    for (int d = 0; d <= i; d++) {
+                        uint32_t b[4];
+                        ldsm4_t(b, at_k(sP + k * kTile, 16 * i, 2 * d, lane));
+                        mma(U[2 * d], oh[i], b[0], b[1]);
+                        mma(U[2 * d + 1], oh[i], b[2], b[3]);
+                    }
             scale_tokens(o, gt + gEG, os, t);
 #pragma unroll
             for (int i = 0; i < 4; i++) split_a(o[2 * i], o[2 * i + 1], 1.f, oh[i], ol[i]);
@@ -746,29 +729,27 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
 #pragma unroll
             for (int n = 0; n < 8; n++) df[32 * n] = make_float4(U[n][0] * oi, U[n][1] * oi, U[n][2] * oi, U[n][3] * oi);
             // Z^T = (exp(G) dO')^T Q
-#pragma unroll 2
-            for (int d = 0; d < KK; d += 2) {
-                float acc[4][4];
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-#pragma unroll
-                    for (int e = 0; e < 4; e++) acc[i][e] = 0.f;
+#pragma unroll 1
+            for (int d = 0; d < KK; d += 4) {
+                float acc[8][4];
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    uint32_t b0[4], b1[4];
-                    ldsm4_t(b0, at_k(sQ, 16 * j, 2 * d, lane));
-                    ldsm4_t(b1, at_k(sQ, 16 * j, 2 * d + 2, lane));
-                    mma(acc[0], oh[j], b0[0], b0[1]);
-                    mma(acc[1], oh[j], b0[2], b0[3]);
-                    mma(acc[2], oh[j], b1[0], b1[1]);
-                    mma(acc[3], oh[j], b1[2], b1[3]);
-                    mma(acc[0], ol[j], b0[0], b0[1]);
-                    mma(acc[1], ol[j], b0[2], b0[3]);
-                    mma(acc[2], ol[j], b1[0], b1[1]);
-                    mma(acc[3], ol[j], b1[2], b1[3]);
+                    uint32_t b[4][4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) ldsm4_t(b[i], at_k(sQ, 16 * j, 2 * (d + i), lane));
+                    if (j == 0) {
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            mma0(acc[2 * i], oh[j], b[i][0], b[i][1]);
+                            mma0(acc[2 * i + 1], oh[j], b[i][2], b[i][3]);
+                        }
+                    } else {
+                        mma_row<0, 4>(acc, oh[j], b);
+                    }
+                    mma_row<0, 4>(acc, ol[j], b);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; i++)
+                for (int i = 0; i < 8; i++)
                     zf[32 * (2 * d + i)] = make_float4(acc[i][0] * oi, acc[i][1] * oi, acc[i][2] * oi, acc[i][3] * oi);
             }
             signal(sh.z_ready + cg, lane);
