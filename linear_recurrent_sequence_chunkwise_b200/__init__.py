@@ -123,6 +123,8 @@ def _load_library():
 
 lib = _load_library()
 
+from . import _binding  # noqa: E402  (the short calls without Python on the way; next to the library, built with it)
+
 
 def ret_last_error_string() -> str:
     return lib.ret_last_error_string().decode(errors="replace")
@@ -683,6 +685,10 @@ def ret_rotary(q, k=None, freqs=None, positions=None, pos_offset: int = 0, layou
     components are taken as they are; pass ``q_out=q`` to work in place.
     ``inverse=True`` is the transpose (the gradient).  Returns the output, or
     the pair of them."""
+    if q_out is k_out is stream is None and freqs is not None and rotary_dim is None and layout in _ROTARY_LAYOUTS:
+        r = _binding.rotary(q, k, freqs, positions, pos_offset, layout == "half", scale, inverse)
+        if r is not None:
+            return r
     if layout not in _ROTARY_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(_ROTARY_LAYOUTS)} (got {layout!r})")
     if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3])):
@@ -735,6 +741,10 @@ def ret_layernorm_forward(x, gain=None, bias=None, eps: float = 1e-5, out=None, 
     """Layer norm over the last dimension of x [..., d]; gain, bias [d] or None.
     Returns the output, or (out, mean, rstd) (fp32, one per row) when the
     statistics are passed in or wanted."""
+    if out is mean is rstd is stream is None:
+        r = _binding.layernorm_forward(x, gain, bias, eps, want_stats)
+        if r is not None:
+            return r
     if x.dim() < 1 or x.numel() == 0:
         raise ValueError("x must be [..., d] with at least one row")
     d, lead = x.shape[-1], x.shape[:-1]
@@ -764,6 +774,10 @@ def ret_layernorm_backward(dout, x, mean, rstd, gain=None, dx=None, dgain=None, 
     """Gradients (dx, dgain, dbias) of ret_layernorm_forward for dout = dL/dout
     and its mean and rstd; dgain and dbias fp32 [d] (None without
     ``want_weights``, unless passed in)."""
+    if dx is dgain is dbias is workspace is stream is None and want_weights:
+        r = _binding.layernorm_backward(dout, x, mean, rstd, gain)
+        if r is not None:
+            return r
     if x.dim() < 1 or x.numel() == 0:
         raise ValueError("x must be [..., d] with at least one row")
     d, lead = x.shape[-1], x.shape[:-1]
@@ -838,6 +852,10 @@ def ret_delta_decode_step(q, k, v, g, beta, state, out=None, out_dtype=None, str
     """One token of the gated delta rule: q, k [B, Hk, dk], v [B, H, dv], g and
     beta [B, H] fp32, state [B, H, dk, dv] fp32 updated in place; returns out
     [B, H, dv]."""
+    if out is stream is None and (out_dtype is None or out_dtype in FLOATS):
+        r = _binding.delta_decode_step(q, k, v, g, beta, state, out_dtype is torch.bfloat16)
+        if r is not None:
+            return r
     (B,), Hk, H, dk, dv = _delta_shapes(q, k, v, g, beta, 1)
     if state is None:
         raise ValueError("state must be float32 [B, H, dk, dv]")

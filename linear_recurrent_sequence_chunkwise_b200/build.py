@@ -1,6 +1,6 @@
 """Build step of the CUDA library: compiles every ``csrc/*.cu`` for sm_100a
-into ``libretention.so`` next to this file (in-tree, so it travels with the
-source tree).  Run as ``python linear_recurrent_sequence_chunkwise_b200/build.py`` (by path:
+into ``libretention.so`` and ``csrc/binding.cpp`` into ``_binding.so`` next to
+this file (in-tree, so they travel with the source tree).  Run as ``python linear_recurrent_sequence_chunkwise_b200/build.py`` (by path:
 importing the package loads the library this script builds)."""
 from __future__ import annotations
 
@@ -12,6 +12,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libretention.so")
+BINDING = os.path.join(HERE, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -33,7 +34,9 @@ def _stale() -> bool:
 
 def build(force: bool = False, verbose: bool = False, jobs: int = 8) -> str:
     """Compile (in parallel, one object per source) and link the shared library."""
+    binding = _start_binding(force)
     if not force and not _stale():
+        _finish_binding(binding)
         return LIB
     objdir = os.path.join(ROOT, "_build", "obj")
     os.makedirs(objdir, exist_ok=True)
@@ -52,7 +55,37 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 8) -> str:
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([NVCC, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp])
     os.replace(tmp, LIB)
+    _finish_binding(binding)
     return LIB
+
+
+def _start_binding(force: bool):
+    """Start compiling the Python binding of the short calls (g++, against torch's headers)."""
+    src, header = os.path.join(HERE, "csrc", "binding.cpp"), os.path.join(ROOT, "include", "retention.h")
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) > max(map(os.path.getmtime, (src, header))):
+        return None
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    inc = [*cpp_extension.include_paths("cuda"), sysconfig.get_path("include"), os.path.join(ROOT, "include")]
+    obj = os.path.join(ROOT, "_build", "obj", "binding.o")
+    os.makedirs(os.path.dirname(obj), exist_ok=True)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-w", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *["-I" + i for i in inc], "-c", src, "-o", obj]
+    return obj, os.path.join(os.path.dirname(torch.__file__), "lib"), \
+        subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _finish_binding(job):
+    if job is None:
+        return
+    obj, torch_lib, p = job
+    _wait(("binding.cpp", p), False)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    # the library next to it; torch's own are loaded by the time it is imported
+    subprocess.check_call(["g++", "-shared", obj, "-o", tmp, "-L" + HERE, "-l:libretention.so", "-L" + torch_lib, "-ltorch_python",
+                           "-ltorch_cuda", "-lc10_cuda", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, BINDING)
 
 
 def _wait(item, verbose):
@@ -61,7 +94,7 @@ def _wait(item, verbose):
     text = out.decode(errors="replace")
     if p.returncode != 0:
         sys.stderr.write(text)
-        raise RuntimeError(f"nvcc failed on {os.path.basename(src)}")
+        raise RuntimeError(f"compiling {os.path.basename(src)} failed")
     if verbose and text.strip():
         sys.stderr.write(f"--- {os.path.basename(src)}\n{text}")
 

@@ -18,8 +18,10 @@
 // exact:
 //   * a key k_i = s_i k'_i with |k'_i| in [1, 2) (a query likewise); the rule for
 //     k' has beta' = beta s^2, v' = v / s, u' = s u, and the same S and G;
-//   * S, R, U (S', Y, U of the gradients) are scaled by the largest value of a
-//     warp's part, and the products of parts are joined in fp32.
+//   * S (and its gradient) is scaled by the largest value of a half of its rows,
+//     R and U (dU and Y) by a bound on theirs: the largest of V' and of S, times
+//     that of beta'.  |X| = |S k'| <= 2 sqrt(dk) max |S|, so such a scale leaves
+//     R below 2^10, and a value 2^-6 of the bound still has its 22 bits.
 // A bf16 output takes one fp16 term of S, U and P (2^-12, against its own 2^-8).
 #pragma once
 
@@ -36,9 +38,10 @@ namespace delta {
 constexpr int C = 64;              // tokens of a chunk
 constexpr int kTile = C * C * 2;   // bytes of a 64 x 64 fp16 tile (128-byte rows, swizzled)
 // Gates of a chunk, 64 values each: in fp32 exp(G), exp(G_C - G), beta', 1 / s
-// of the keys, s of the queries; then G in 64 bits.
-constexpr int gEG = 0, gEC = C, gBeta = 2 * C, gIk = 3 * C, gSq = 4 * C;
-constexpr int kGates = 5 * C * 4;
+// of the keys, s of the queries, the largest |beta'| of each half; then G in 64
+// bits.
+constexpr int gEG = 0, gEC = C, gBeta = 2 * C, gIk = 3 * C, gSq = 4 * C, gMax = 5 * C;
+constexpr int kGates = 5 * C * 4 + 16;
 constexpr int kGateRow = kGates + C * 8;
 // Below this a decay is zero in fp32; keeps -inf out of the sums.
 constexpr float kMinG = -128.f;
@@ -179,6 +182,12 @@ __device__ __forceinline__ float scale_for(float m, float& inverse) {
     inverse = __int_as_float((254 - s) << 23);
     return __int_as_float(s << 23);
 }
+// The same for a bound: into [8, 16).
+__device__ __forceinline__ float bound_scale(float m, float& inverse) {
+    const float s = scale_for(m, inverse);
+    inverse *= 0.5f;
+    return 2.f * s;
+}
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
@@ -212,13 +221,13 @@ ret_status launch_prep(const DeltaArgs& a, const Tables& t, cudaStream_t s);
 //   u   [hi, lo][16][64]         the corrections U'
 //   y   the same                 dY = T^T dU
 //   o   [16][64]                 dO' = s_q dO, one term
-//   f   5 fp32: the inverse scales of s, ds, u, y, o
+//   f   7 fp32: the inverse scales of s and ds (a half of dk each), u, y, o
 template <int DK>
 struct Record {
     static constexpr int s = 0, ds = 64 * DK, u = 128 * DK, y = u + 4096, o = y + 4096, f = o + 2048, bytes = f + 128;
 };
 inline size_t record_bytes(int dk) { return 128 * (size_t)dk + 4096 * 2 + 2048 + 128; }
-enum : int { fS = 0, fDs = 1, fU = 2, fY = 3, fO = 4 };
+enum : int { fS = 0, fDs = 2, fU = 4, fY = 5, fO = 6 };
 __host__ __device__ __forceinline__ int groups_of(int dv) { return (dv + 15) / 16; }
 ret_status launch_chains(const DeltaArgs& a, const Tables& t, uint8_t* records, cudaStream_t s);
 

@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
                     add_scaled(W[i], y, iy * iu);
                 }
             }
-            const float is = f[fS], id = f[fDs];
+            const float is = f[fS + cg / 2], id = f[fDs + cg / 2];
 #pragma unroll
             for (int p = 0; p < DW / 16; p++) {
                 uint32_t bh[4], bl[4], dh[4], dl[4];
@@ -255,14 +255,16 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
                     add_scaled(Zw[2 * p + i], z, iu * id);
                 }
             }
-            // <dS1, S0>: pairs tid, tid + 512, ... of the group's 16 dk values
+            // <dS1, S0> of the share's columns, four of the 16 rows each
             {
                 float x = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8 * DK / Gr::threads; i++) {
-                    const uint8_t *q = rec + Rec::s + 4 * (tid + i * Gr::threads), *u = q + (Rec::ds - Rec::s);
-                    const float2 s2 = sum_h2(*reinterpret_cast<const uint32_t*>(q), *reinterpret_cast<const uint32_t*>(q + 32 * DK));
-                    const float2 d2 = sum_h2(*reinterpret_cast<const uint32_t*>(u), *reinterpret_cast<const uint32_t*>(u + 32 * DK));
+                for (int i = 0; i < DW / 16; i++) {
+                    const int q = i * 32 + lane;  // of the DW / 2 pairs of four rows
+                    const uint32_t off = tile_at<16>(4 * rg + q / (DW / 2), (cg * DW + 2 * (q % (DW / 2))) / 8) + 4 * (q & 3);
+                    const uint8_t *ps = rec + Rec::s + off, *pd = rec + Rec::ds + off;
+                    const float2 s2 = sum_h2(*reinterpret_cast<const uint32_t*>(ps), *reinterpret_cast<const uint32_t*>(ps + 32 * DK));
+                    const float2 d2 = sum_h2(*reinterpret_cast<const uint32_t*>(pd), *reinterpret_cast<const uint32_t*>(pd + 32 * DK));
                     x = fmaf(s2.x, d2.x, x);
                     x = fmaf(s2.y, d2.y, x);
                 }

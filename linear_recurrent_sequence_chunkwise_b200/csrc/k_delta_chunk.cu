@@ -4,15 +4,19 @@
 //
 // What bounds it is the chain: chunk c + 1 needs the state of chunk c, and a
 // (sequence, head) has only its value columns to share out, which do not
-// depend on each other.  Sixteen columns are the work of two warps.
-// The first, the chain warp, carries them through the recurrence without a
-// barrier: it holds the transposed state [16 x dk] as fp32 accumulator tiles,
-// whose layout is that of the A operand of the next product (X^T = S^T K^T,
-// U^T = R^T T^T, S^T += U^T K), so nothing it computes leaves its registers on
-// the way.  Everything that the recurrence does not wait for is its helper's,
-// on the same SM sub-partition, which fills the tensor pipe while the chain
-// warp converts: the outputs (Q S and P U), or in the backward pass the terms
-// of dO and the records.  The two hand over operand tiles through shared memory.
+// depend on each other.  Sixteen columns are the work of three warps.
+// Two chain warps carry them through the recurrence: each holds half of dk of
+// the transposed state, [16 x dk/2] as fp32 accumulator tiles, whose layout is
+// that of the A operand of the next product (X^T = S^T K^T, U^T = R^T T^T,
+// S^T += U^T K), and owns two of the four quarters of the chunk's tokens between
+// the products over dk (the first and the last, or the two between: T is
+// triangular, so both have the same work).  They exchange parts of X, R and U
+// through shared memory, with three barriers of 64 threads in a chunk; one warp
+// alone takes 8,700 clocks for a chunk of dk = 128, of which the tensor pipe
+// needs 2,600, and two such warps on a sub-partition fill each other's gaps.
+// Everything that the recurrence does not wait for is the third warp's, the
+// helper: the outputs (Q S and P U), or in the backward pass the terms of dO
+// and the records.  It gets the operand tiles of S and U as they are.
 // The products run as mma.sync, not tcgen05: every operand is split into two
 // fp16 terms between two products, in registers at once, where TMEM would cost
 // a trip out and back for each of the four products of a chunk.
@@ -47,23 +51,25 @@ enum : int { kOutBf16 = 0, kOutF32 = 1, kKeep = 2, kBack = 3 };
 // Shared memory of a block of CG groups of 16 columns.
 template <int DK, int CG, int MODE>
 struct Plan {
-    static constexpr int warps = 2 * CG;
-    // a stage: K' (then Q'), T (then P), the gates
-    static constexpr int keys = 2 * C * DK * (MODE == kKeep ? 1 : 2);
-    static constexpr int tiles = MODE == kKeep ? 2 * kTile : MODE == kOutBf16 ? 3 * kTile : 4 * kTile;
-    static constexpr int oT = keys, oGate = keys + tiles, stage = oGate + 2048;
-    static constexpr uint32_t loaded = keys + tiles + kGates;
+    static constexpr int warps = 3 * CG;  // 2 CG of the chains, then CG helpers
+    // Two rings: the chain warps' K', T and gates, and the helpers' Q', P and gates.
+    static constexpr int kGateRoom = 1536, keys = 2 * C * DK;
+    static constexpr int oT = keys, aGate = oT + 2 * kTile, A = aGate + kGateRoom;
+    static constexpr int pTiles = MODE == kOutBf16 ? kTile : 2 * kTile;
+    static constexpr int oP = keys, bGate = oP + pTiles, B = MODE == kKeep ? 0 : bGate + kGateRoom;
     // a group's: S in one or two terms, U (Y) the same way, staging of 64 x 16
-    // bf16; the backward: Z in fp32, dU0 in fp32
+    // bf16; between the chain warps parts of X, in whose place each later puts
+    // its R (dU), and exp(G_C - G) U (exp(G) beta' Y); the backward: Z in fp32,
+    // dU0 in fp32
     static constexpr int terms = MODE == kOutBf16 ? 1 : 2;
     static constexpr int sHalf = DK / 16 * 512, oU = terms * sHalf, uHalf = 4 * 512, oV = oU + terms * uHalf;
-    static constexpr int oZ = oV + 2048, oD = oZ + (MODE == kBack ? DK * 64 : 0);
+    static constexpr int oX = oV + 2048, oE = oX + 4096;
+    static constexpr int oZ = oE + 4096, oD = oZ + (MODE == kBack ? DK * 64 : 0);
     static constexpr int group = oD + (MODE == kBack ? 4096 : 0);
-    static constexpr int most = 226 * 1024 - 1024 - 512;
-    static constexpr int fit = (most - CG * group) / stage;
-    static constexpr int NS = fit > 3 ? 3 : fit;
-    static_assert(NS >= 1, "tiles and exchange buffers exceed shared memory");
-    static constexpr int oG = NS * stage, oBar = oG + CG * group;
+    static constexpr int most = 226 * 1024 - 1024 - 512, left = most - CG * group;
+    static constexpr int NA = 2 * A + B <= left ? 2 : 1, NB = NA * A + 2 * B <= left ? 2 : 1;
+    static_assert(NA * A + NB * B <= left, "tiles and exchange buffers exceed shared memory");
+    static constexpr int oB = NA * A, oG = oB + NB * B, oBar = oG + CG * group;
     static constexpr int smem = oBar + 512 + 1024;
 };
 
@@ -98,42 +104,56 @@ __device__ __forceinline__ void signal(uint64_t* bar, int lane) {
 // pair (ready, free) for the tiles of S, those of U and the helper's fp32 terms.
 struct Shared {
     uint8_t* sm;
-    uint64_t *full, *empty, *s_ready, *s_free, *u_ready, *u_free, *z_ready, *z_free;
-    float *s_inv, *u_inv;
+    uint64_t *fa, *ea, *fb, *eb, *s_ready, *s_free, *u_ready, *u_free, *z_ready, *z_free;
+    float *s_inv, *u_inv, *s_max, *v_max;  // [2] a group, u_inv one
     template <typename Pl, int CG>
     __device__ __forceinline__ void init() {
         extern __shared__ uint8_t raw[];
         sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-        full = reinterpret_cast<uint64_t*>(sm + Pl::oBar);
-        empty = full + 3, s_ready = empty + 3, s_free = s_ready + 4, u_ready = s_free + 4, u_free = u_ready + 4;
+        fa = reinterpret_cast<uint64_t*>(sm + Pl::oBar);
+        ea = fa + 2, fb = ea + 2, eb = fb + 2, s_ready = eb + 2, s_free = s_ready + 4, u_ready = s_free + 4, u_free = u_ready + 4;
         z_ready = u_free + 4, z_free = z_ready + 4;
         s_inv = reinterpret_cast<float*>(z_free + 4);
-        u_inv = s_inv + 4;
+        u_inv = s_inv + 8, s_max = u_inv + 4, v_max = s_max + 8;
         if (threadIdx.x == 0) {
-            for (int i = 0; i < Pl::NS; i++) {
-                tc::mbar_init(full + i, 1);
-                tc::mbar_init(empty + i, Pl::warps);
+            for (int i = 0; i < 2; i++) {
+                tc::mbar_init(fa + i, 1), tc::mbar_init(fb + i, 1);
+                tc::mbar_init(ea + i, 2 * CG), tc::mbar_init(eb + i, CG);
             }
-            for (int i = 0; i < CG; i++)
-                for (uint64_t* b : {s_ready, s_free, u_ready, u_free, z_ready, z_free}) tc::mbar_init(b + i, 1);
+            for (int i = 0; i < CG; i++) {
+                for (uint64_t* b : {s_free, u_free, z_ready}) tc::mbar_init(b + i, 1);
+                for (uint64_t* b : {s_ready, u_ready, z_free}) tc::mbar_init(b + i, 2);
+            }
             tc::fence_barrier_init();
         }
         __syncthreads();
     }
 };
 
-// One lane: chunk c of the sequence into its stage.
+// One lane: the tiles of a chunk, the it-th that is walked, into the rings.
 template <typename Pl, int DK>
-__device__ __forceinline__ void load_stage(const Shared& r, const ChainArgs& a, size_t key_chunk, size_t chunk, int it,
-                                           Waits& wait) {
-    if (it >= Pl::NS) wait(r.empty + it % Pl::NS, it / Pl::NS - 1);
+__device__ __forceinline__ void load_a(const Shared& r, const ChainArgs& a, size_t key_chunk, size_t chunk, int it,
+                                       Waits& wait) {
+    if (it >= Pl::NA) wait(r.ea + it % Pl::NA, it / Pl::NA - 1);
     if (!wait.ok) return;
-    uint8_t* s = r.sm + (it % Pl::NS) * Pl::stage;
-    uint64_t* bar = r.full + it % Pl::NS;
-    tc::mbar_arrive_expect_tx(bar, Pl::loaded);
+    uint8_t* s = r.sm + (it % Pl::NA) * Pl::A;
+    uint64_t* bar = r.fa + it % Pl::NA;
+    tc::mbar_arrive_expect_tx(bar, Pl::keys + 2 * kTile + kGates);
     bulk_load(s, a.tb.keys + key_chunk * (4 * C * DK), Pl::keys, bar);
-    bulk_load(s + Pl::oGate, a.tb.gates + chunk * kGateRow, kGates, bar);
-    bulk_load(s + Pl::oT, a.tb.tiles + chunk * 4 * kTile, Pl::tiles, bar);
+    bulk_load(s + Pl::aGate, a.tb.gates + chunk * kGateRow, kGates, bar);
+    bulk_load(s + Pl::oT, a.tb.tiles + chunk * 4 * kTile, 2 * kTile, bar);
+}
+template <typename Pl, int DK>
+__device__ __forceinline__ void load_b(const Shared& r, const ChainArgs& a, size_t key_chunk, size_t chunk, int it,
+                                       Waits& wait) {
+    if (it >= Pl::NB) wait(r.eb + it % Pl::NB, it / Pl::NB - 1);
+    if (!wait.ok) return;
+    uint8_t* s = r.sm + Pl::oB + (it % Pl::NB) * Pl::B;
+    uint64_t* bar = r.fb + it % Pl::NB;
+    tc::mbar_arrive_expect_tx(bar, Pl::keys + Pl::pTiles + kGates);
+    bulk_load(s, a.tb.keys + key_chunk * (4 * C * DK) + Pl::keys, Pl::keys, bar);
+    bulk_load(s + Pl::oP, a.tb.tiles + chunk * 4 * kTile + 2 * kTile, Pl::pTiles, bar);
+    bulk_load(s + Pl::bGate, a.tb.gates + chunk * kGateRow, kGates, bar);
 }
 
 __device__ __forceinline__ void put4(uint8_t* p, const uint32_t (&r)[4], int lane) {
@@ -144,15 +164,63 @@ __device__ __forceinline__ void get4(const uint8_t* p, uint32_t (&r)[4], int lan
     r[0] = u.x, r[1] = u.y, r[2] = u.z, r[3] = u.w;
 }
 
-// The scale of a warp's tiles.
+// The largest magnitude of a warp's tiles, and the scale for it.
 template <int N>
-__device__ __forceinline__ float tiles_scale(const float (&S)[N][4], float& inverse) {
+__device__ __forceinline__ float tiles_max(const float (&S)[N][4]) {
     float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int n = 0; n < N; n++)
 #pragma unroll
         for (int e = 0; e < 4; e++) m[e] = fmaxf(m[e], fabsf(S[n][e]));
-    return scale_for(warp_max(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]))), inverse);
+    return warp_max(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+}
+template <int N>
+__device__ __forceinline__ float tiles_scale(const float (&S)[N][4], float& inverse) {
+    return scale_for(tiles_max(S), inverse);
+}
+// The parts of a product over dk: the other warp's quarters (its first and
+// second) go to it, the own ones (hf and 3 - hf) are returned.
+__device__ __forceinline__ void hand_over(uint8_t* buf, const float (&x)[8][4], int hf, float s, int lane, float (&mine)[4][4]) {
+    float4* dst = reinterpret_cast<float4*>(buf + (1 - hf) * 2048) + lane;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        // tiles of quarters 0, 3 (hf 0) and 1, 2 (hf 1), in that order
+        const int t0 = i < 2 ? i : 4 + i, t1 = 2 + i;
+        const float(&give)[4] = hf ? x[t0] : x[t1];
+        const float(&keep)[4] = hf ? x[t1] : x[t0];
+        dst[32 * i] = make_float4(give[0] * s, give[1] * s, give[2] * s, give[3] * s);
+#pragma unroll
+        for (int e = 0; e < 4; e++) mine[i][e] = keep[e] * s;
+    }
+}
+__device__ __forceinline__ void take_over(const uint8_t* buf, int hf, int lane, float (&mine)[4][4]) {
+    const float4* src = reinterpret_cast<const float4*>(buf + hf * 2048) + lane;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float4 y = src[32 * i];
+        mine[i][0] += y.x, mine[i][1] += y.y, mine[i][2] += y.z, mine[i][3] += y.w;
+    }
+}
+// acc = sum over the tokens of (hi + lo)^T B, B's 16 D columns from piece 2 d on.
+template <int D>
+__device__ __forceinline__ void state_product(float (&acc)[8][4], const uint32_t (&hi)[4][4], const uint32_t (&lo)[4][4],
+                                              uint32_t sB, int d, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        uint32_t b[4][4];
+#pragma unroll
+        for (int i = 0; i < D; i++) ldsm4_t(b[i], at_k(sB, 16 * j, 2 * (d + i), lane));
+        if (j == 0) {
+#pragma unroll
+            for (int i = 0; i < D; i++) {
+                mma0(acc[2 * i], hi[j], b[i][0], b[i][1]);
+                mma0(acc[2 * i + 1], hi[j], b[i][2], b[i][3]);
+            }
+        } else {
+            mma_row<0, D>(acc, hi[j], b);
+        }
+        mma_row<0, D>(acc, lo[j], b);
+    }
 }
 template <int N>
 __device__ __forceinline__ void zero(float (&x)[N][4]) {
@@ -234,7 +302,7 @@ __device__ __forceinline__ void keep_tile(uint8_t* rec, int piece, int lane, con
 template <int DK, int CG, int MODE>
 __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
     using Pl = Plan<DK, CG, MODE>;
-    constexpr int NS = Pl::NS, KK = DK / 16;
+    constexpr int NA = Pl::NA, NB = Pl::NB, KK = DK / 16;
     Shared sh;
     sh.init<Pl, CG>();
     const int h = blockIdx.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -246,137 +314,171 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
     uint8_t *sf = ex, *uf = ex + Pl::oU, *slot = ex + Pl::oV;
     Waits wait;
 
-    if (w < CG) {  // the chain
-        const size_t sb = ((size_t)b * a.H + h) * DK * a.dv;
-        float S[DK / 8][4];
+    if (w < 2 * CG) {  // the chain: half `hf` of dk, quarters qa and qb of the tokens
+        constexpr int KH = KK / 2;
+        const int hf = w / CG, qa = hf, qb = 3 - hf;
+        const size_t sb = (((size_t)b * a.H + h) * DK + hf * (DK / 2)) * a.dv;
+        float S[DK / 16][4];
         read_state(S, a.initial_state ? a.initial_state + sb : nullptr, a.dv, col0 + g, t);
         const Rows vrows = rows_at(a.v, a, b, h, col0 + 8 * (lane & 1), len);
-        uint4 vn[4];
-        if (n_chunks)
-#pragma unroll
-            for (int i = 0; i < 4; i++) vn[i] = vrows.load(16 * i + (lane >> 1));
+        const int tok_a = 16 * qa + (lane >> 1), tok_b = 16 * qb + (lane >> 1);
+        uint4 va = make_uint4(0, 0, 0, 0), vb = va;
+        if (n_chunks) va = vrows.load(tok_a), vb = vrows.load(tok_b);
+        float m_own = tiles_max(S);
+        uint8_t *xf = ex + Pl::oX, *ef = ex + Pl::oE;
+        // R of quarter q, in its owner's part of the exchange of X: quarters 0, 3, 1, 2
+        auto rf = [&](int q) { return xf + (q == 0 ? 0 : q == 3 ? 1024 : q == 1 ? 2048 : 3072); };
         for (int c = 0; c < n_chunks; c++) {
-            uint8_t* st = sh.sm + (c % NS) * Pl::stage;
+            uint8_t* st = sh.sm + (c % NA) * Pl::A;
             const uint32_t sK = tc::smem_u32(st), sT = sK + Pl::oT;
-            const float* gt = reinterpret_cast<const float*>(st + Pl::oGate);
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                *reinterpret_cast<uint4*>(slot + 512 * i + 16 * lane) = vrows.use(vn[i], c * C + 16 * i + (lane >> 1));
-#pragma unroll
-            for (int i = 0; i < 4; i++) vn[i] = vrows.load((c + 1) * C + 16 * i + (lane >> 1));
+            const float* gt = reinterpret_cast<const float*>(st + Pl::aGate);
+            // V of the own quarters, transposed
+            uint32_t v4[2][4];
+            transpose16(slot + 512 * qa, vrows.use(va, c * C + tok_a), lane, v4[0]);
+            transpose16(slot + 512 * qb, vrows.use(vb, c * C + tok_b), lane, v4[1]);
+            va = vrows.load((c + 1) * C + tok_a);
+            vb = vrows.load((c + 1) * C + tok_b);
 
-            // X^T = S^T K^T; the helper gets the operand tiles
-            float inv;
-            const float ss = tiles_scale(S, inv);
-            const float si = inv;
+            // the half's X^T = S^T K^T; the helper gets the operand tiles
+            float si;
+            const float ss = scale_for(m_own, si);
             float X[8][4];
             zero(X);
-            wait(sh.full + c % NS, c / NS);
+            wait(sh.fa + c % NA, c / NA);
             if (c > 0) wait(sh.s_free + cg, c - 1);
 #pragma unroll
-            for (int kk = 0; kk < KK; kk++) {
+            for (int kk = 0; kk < KH; kk++) {
                 uint32_t hi[4], lo[4];
                 split_a(S[2 * kk], S[2 * kk + 1], ss, hi, lo);
-                put4(sf + kk * 512, hi, lane);
-                if constexpr (Pl::terms == 2) put4(sf + Pl::sHalf + kk * 512, lo, lane);
+                put4(sf + (hf * KH + kk) * 512, hi, lane);
+                if constexpr (Pl::terms == 2) put4(sf + Pl::sHalf + (hf * KH + kk) * 512, lo, lane);
                 uint32_t bk[4][4];
 #pragma unroll
-                for (int p = 0; p < 4; p++) ldsm4(bk[p], at_n(sK, 16 * p, 2 * kk, lane));
+                for (int p = 0; p < 4; p++) ldsm4(bk[p], at_n(sK, 16 * p, 2 * (hf * KH + kk), lane));
                 mma_row<0, 4>(X, hi, bk);
                 mma_row<0, 4>(X, lo, bk);
             }
-            if (lane == 0) sh.s_inv[cg] = si;
-            signal(sh.s_ready + cg, lane);
-
-            // R^T = beta' (V' - exp(G) X)
+            // V' of the own quarters and its largest value
+            float vq[4][4], vm = 0.f;
 #pragma unroll
-            for (int p = 0; p < 4; p++) {
-                uint32_t v4[4];
-                const int m = lane >> 3, tok = 8 * (m >> 1) + (lane & 7);
-                ldsm4_t(v4, tc::smem_u32(slot) + 512 * p + tok * 32 + (m & 1) * 16);
+            for (int n = 0; n < 4; n++) {
+                const float2 ik = *reinterpret_cast<const float2*>(gt + gIk + 16 * (n < 2 ? qa : qb) + 8 * (n & 1) + 2 * t);
+                const uint32_t x = v4[n / 2][2 * (n & 1)], y = v4[n / 2][2 * (n & 1) + 1];
+                vq[n][0] = tc::bf16lo(x) * ik.x, vq[n][1] = tc::bf16hi(x) * ik.y;
+                vq[n][2] = tc::bf16lo(y) * ik.x, vq[n][3] = tc::bf16hi(y) * ik.y;
 #pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const int n = 2 * p + i, at = 8 * n + 2 * t;
-                    float2 eg = *reinterpret_cast<const float2*>(gt + gEG + at);
-                    const float2 bt = *reinterpret_cast<const float2*>(gt + gBeta + at);
-                    const float2 ik = *reinterpret_cast<const float2*>(gt + gIk + at);
-                    eg.x *= -si, eg.y *= -si;
-                    X[n][0] = bt.x * fmaf(eg.x, X[n][0], tc::bf16lo(v4[2 * i]) * ik.x);
-                    X[n][1] = bt.y * fmaf(eg.y, X[n][1], tc::bf16hi(v4[2 * i]) * ik.y);
-                    X[n][2] = bt.x * fmaf(eg.x, X[n][2], tc::bf16lo(v4[2 * i + 1]) * ik.x);
-                    X[n][3] = bt.y * fmaf(eg.y, X[n][3], tc::bf16hi(v4[2 * i + 1]) * ik.y);
-                }
+                for (int e = 0; e < 4; e++) vm = fmaxf(vm, fabsf(vq[n][e]));
             }
-            const float rs = tiles_scale(X, inv);
-            const float ri = inv;
+            vm = warp_max(vm);
+            if (lane == 0) {
+                sh.s_inv[2 * cg + hf] = si;
+                sh.s_max[2 * cg + hf] = m_own;
+                sh.v_max[2 * cg + hf] = vm;
+            }
+            signal(sh.s_ready + cg, lane);
+            float R[4][4];  // quarters qa, qb
+            hand_over(xf, X, hf, si, lane, R);
+            tc::barrier(1 + cg, 64);
+            take_over(xf, hf, lane, R);
+
+            // R^T = beta' (V' - exp(G) X); one scale for R and U of the group
+            const float bound = fmaxf(fmaxf(sh.v_max[2 * cg], sh.v_max[2 * cg + 1]), fmaxf(sh.s_max[2 * cg], sh.s_max[2 * cg + 1])) *
+                                fmaxf(1.f, fmaxf(gt[gMax], gt[gMax + 1]));
+            float ui;
+            const float us = bound_scale(bound, ui);
+#pragma unroll
+            for (int n = 0; n < 4; n++) {
+                const int at = 16 * (n < 2 ? qa : qb) + 8 * (n & 1) + 2 * t;
+                const float2 eg = *reinterpret_cast<const float2*>(gt + gEG + at);
+                const float2 bt = *reinterpret_cast<const float2*>(gt + gBeta + at);
+                R[n][0] = bt.x * (vq[n][0] - eg.x * R[n][0]);
+                R[n][1] = bt.y * (vq[n][1] - eg.y * R[n][1]);
+                R[n][2] = bt.x * (vq[n][2] - eg.x * R[n][2]);
+                R[n][3] = bt.y * (vq[n][3] - eg.y * R[n][3]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                uint32_t hi[4], lo[4];
+                const int q = i ? qb : qa;
+                split_a(R[2 * i], R[2 * i + 1], us, hi, lo);
+                put4(rf(q), hi, lane);
+                put4(rf(q) + 512, lo, lane);
+            }
+            tc::barrier(1 + cg, 64);
 
             // U^T = R^T T^T; T is lower triangular: token i takes j <= i
-            float U[8][4];
+            float U[4][4];
             zero(U);
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                uint32_t rh[4], rl[4];
-                split_a(X[2 * j], X[2 * j + 1], rs, rh, rl);
-                uint32_t th[4][4], tl[4][4];
+                if (j > qb) continue;
+                uint32_t rh[4], rl[4], th[2][4], tl[2][4];
+                get4(rf(j), rh, lane);
+                get4(rf(j) + 512, rl, lane);
 #pragma unroll
-                for (int p = j; p < 4; p++) {
-                    ldsm4(th[p], at_n(sT, 16 * p, 2 * j, lane));
-                    ldsm4(tl[p], at_n(sT + kTile, 16 * p, 2 * j, lane));
-                }
+                for (int i = 0; i < 2; i++)
+                    if (i || j <= qa) {
+                        ldsm4(th[i], at_n(sT, 16 * (i ? qb : qa), 2 * j, lane));
+                        ldsm4(tl[i], at_n(sT + kTile, 16 * (i ? qb : qa), 2 * j, lane));
+                    }
 #pragma unroll
                 for (int k = 0; k < 3; k++)
 #pragma unroll
-                    for (int p = j; p < 4; p++) {
-                        const uint32_t(&b)[4] = k == 2 ? tl[p] : th[p];
-                        mma(U[2 * p], k == 1 ? rl : rh, b[0], b[1]);
-                        mma(U[2 * p + 1], k == 1 ? rl : rh, b[2], b[3]);
-                    }
+                    for (int i = 0; i < 2; i++)
+                        if (i || j <= qa) {
+                            const uint32_t(&x)[4] = k == 2 ? tl[i] : th[i];
+                            mma(U[2 * i], k == 1 ? rl : rh, x[0], x[1]);
+                            mma(U[2 * i + 1], k == 1 ? rl : rh, x[2], x[3]);
+                        }
             }
-            float ui = 0.f;
-            const float us = tiles_scale(U, ui);  // of ri-scaled values: U is still times rs
-            ui *= ri;
             if (c > 0) wait(sh.u_free + cg, c - 1);
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                uint32_t uh[4], ul[4];
-                split_a(U[2 * j], U[2 * j + 1], us, uh, ul);
-                put4(uf + j * 512, uh, lane);
-                if constexpr (Pl::terms == 2) put4(uf + Pl::uHalf + j * 512, ul, lane);
+            for (int i = 0; i < 2; i++) {
+                uint32_t hi[4], lo[4];
+                const int q = i ? qb : qa;
+                // exp(G_C - G) U for the state, U for the helper
+                float E[2][4];
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    const float2 e2 = *reinterpret_cast<const float2*>(gt + gEC + 16 * q + 8 * k + 2 * t);
+                    E[k][0] = U[2 * i + k][0] * e2.x, E[k][1] = U[2 * i + k][1] * e2.y;
+                    E[k][2] = U[2 * i + k][2] * e2.x, E[k][3] = U[2 * i + k][3] * e2.y;
+                }
+                split_a(E[0], E[1], 1.f, hi, lo);
+                put4(ef + q * 1024, hi, lane);
+                put4(ef + q * 1024 + 512, lo, lane);
+                split_a(U[2 * i], U[2 * i + 1], 1.f, hi, lo);
+                put4(uf + q * 512, hi, lane);
+                if constexpr (Pl::terms == 2) put4(uf + Pl::uHalf + q * 512, lo, lane);
             }
-            if (lane == 0) sh.u_inv[cg] = ui;
+            if (lane == 0 && hf == 0) sh.u_inv[cg] = ui;
             signal(sh.u_ready + cg, lane);
+            tc::barrier(1 + cg, 64);
 
-            // S^T <- exp(G_C) S^T + (exp(G_C - G) U)^T K
+            // the half's S^T <- exp(G_C) S^T + (exp(G_C - G) U)^T K
             const float eC = gt[gEG + C - 1];
-            scale_tokens(U, gt + gEC, us, t);
             uint32_t uh[4][4], ul[4][4];
 #pragma unroll
-            for (int j = 0; j < 4; j++) split_a(U[2 * j], U[2 * j + 1], 1.f, uh[j], ul[j]);
-#pragma unroll
-            for (int d = 0; d < KK; d += 4) {
-                float acc[8][4];
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    uint32_t b[4][4];
-#pragma unroll
-                    for (int i = 0; i < 4; i++) ldsm4_t(b[i], at_k(sK, 16 * j, 2 * (d + i), lane));
-                    if (j == 0) {
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            mma0(acc[2 * i], uh[j], b[i][0], b[i][1]);
-                            mma0(acc[2 * i + 1], uh[j], b[i][2], b[i][3]);
-                        }
-                    } else {
-                        mma_row<0, 4>(acc, uh[j], b);
-                    }
-                    mma_row<0, 4>(acc, ul[j], b);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-#pragma unroll
-                    for (int e = 0; e < 4; e++) S[2 * d + i][e] = fmaf(ui, acc[i][e], eC * S[2 * d + i][e]);
+            for (int j = 0; j < 4; j++) {
+                get4(ef + j * 1024, uh[j], lane);
+                get4(ef + j * 1024 + 512, ul[j], lane);
             }
-            signal(sh.empty + c % NS, lane);
+            float m[4] = {0.f, 0.f, 0.f, 0.f};
+            constexpr int D = KH < 4 ? KH : 4;
+#pragma unroll
+            for (int d = 0; d < KH; d += D) {
+                float acc[8][4];
+                state_product<D>(acc, uh, ul, sK, hf * KH + d, lane);
+#pragma unroll
+                for (int i = 0; i < 2 * D; i++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        S[2 * d + i][e] = fmaf(ui, acc[i][e], eC * S[2 * d + i][e]);
+                        m[e] = fmaxf(m[e], fabsf(S[2 * d + i][e]));
+                    }
+            }
+            signal(sh.ea + c % NA, lane);
+            m_own = warp_max(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
         }
         if (a.final_state) write_state(S, a.final_state + sb, a.dv, col0 + g, t);
         return;
@@ -385,14 +487,18 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
     // the helper; the first one also feeds the stages
     const int hk = h / (a.H / a.Hk);
     const size_t kc0 = ((size_t)b * a.Hk + hk) * a.nc;
-    const bool feeds = w == CG && lane == 0;
+    const bool feeds = w == 2 * CG && lane == 0;
     if (feeds)
-        for (int c = 0; c < NS - 1 && c < n_chunks; c++) load_stage<Pl, DK>(sh, a, kc0 + c, ch0 + c, c, wait);
+        for (int c = 0; c < NA - 1 && c < n_chunks; c++) load_a<Pl, DK>(sh, a, kc0 + c, ch0 + c, c, wait);
+    if (MODE != kKeep && feeds)
+        for (int c = 0; c < NB - 1 && c < n_chunks; c++) load_b<Pl, DK>(sh, a, kc0 + c, ch0 + c, c, wait);
     for (int c = 0; c < n_chunks; c++) {
-        if (feeds && c + NS - 1 < n_chunks)
-            load_stage<Pl, DK>(sh, a, kc0 + c + NS - 1, ch0 + c + NS - 1, c + NS - 1, wait);
+        if (feeds) {
+            const int na = c + NA - 1, nb = c + NB - 1;
+            if (MODE != kKeep && nb < n_chunks) load_b<Pl, DK>(sh, a, kc0 + nb, ch0 + nb, nb, wait);
+            if (na < n_chunks) load_a<Pl, DK>(sh, a, kc0 + na, ch0 + na, na, wait);
+        }
         __syncwarp();
-        uint8_t* st = sh.sm + (c % NS) * Pl::stage;
         if constexpr (MODE == kKeep) {
             // the operand tiles into the chunk's record
             uint8_t* rec = a.records + ((ch0 + c) * groups_of(a.dv) + group) * Record<DK>::bytes;
@@ -408,7 +514,7 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                     get4(sf + Pl::sHalf + kk * 512, r, lane);
                     keep_tile(rec + Record<DK>::s + 32 * DK, 2 * kk, lane, r);
                 }
-                if (lane == 0) rf[fS] = sh.s_inv[cg];
+                if (lane < 2) rf[fS + lane] = sh.s_inv[2 * cg + lane];
             }
             signal(sh.s_free + cg, lane);
             wait(sh.u_ready + cg, c);
@@ -427,14 +533,22 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
         } else {
             // O^T = s_q (exp(G) S^T Q^T + U^T P^T).  A bf16 output takes one term
             // of S, U and P (off by 2^-12 at most each, against its own 2^-9).
-            const uint32_t sQ = tc::smem_u32(st) + 2 * C * DK, sP = tc::smem_u32(st) + Pl::oT + 2 * kTile;
-            const float* gt = reinterpret_cast<const float*>(st + Pl::oGate);
+            uint8_t* st = sh.sm + Pl::oB + (c % NB) * Pl::B;
+            const uint32_t sQ = tc::smem_u32(st), sP = sQ + Pl::oP;
+            const float* gt = reinterpret_cast<const float*>(st + Pl::bGate);
             float O[8][4];
             zero(O);
-            wait(sh.full + c % NS, c / NS);
+            wait(sh.fb + c % NB, c / NB);
             wait(sh.s_ready + cg, c);
+            const float s0 = sh.s_inv[2 * cg], si = sh.s_inv[2 * cg + 1];
 #pragma unroll 4
             for (int kk = 0; kk < KK; kk++) {
+                if (kk == KK / 2) {  // the halves have their own scales
+#pragma unroll
+                    for (int n = 0; n < 8; n++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++) O[n][e] *= s0 / si;
+                }
                 uint32_t hi[4], lo[4];
                 get4(sf + kk * 512, hi, lane);
                 if constexpr (Pl::terms == 2) get4(sf + Pl::sHalf + kk * 512, lo, lane);
@@ -444,7 +558,6 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                 mma_row<0, 4>(O, hi, bq);
                 if constexpr (Pl::terms == 2) mma_row<0, 4>(O, lo, bq);
             }
-            const float si = sh.s_inv[cg];
             signal(sh.s_free + cg, lane);
             wait(sh.u_ready + cg, c);
             const float ui = sh.u_inv[cg];
@@ -472,6 +585,7 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                 }
             }
             scale_tokens(O, gt + gSq, ui, t);
+            signal(sh.eb + c % NB, lane);
             const size_t row0 = (size_t)b * a.N + (size_t)c * C;
             const int L = len - c * C;
             if constexpr (MODE == kOutF32) {
@@ -512,7 +626,6 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                 }
             }
         }
-        signal(sh.empty + c % NS, lane);
     }
 }
 
@@ -527,7 +640,7 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
 template <int DK, int CG>
 __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* dfinal, float* dinitial, int b) {
     using Pl = Plan<DK, CG, kBack>;
-    constexpr int NS = Pl::NS, KK = DK / 16;
+    constexpr int NA = Pl::NA, NB = Pl::NB, KK = DK / 16;
     Shared sh;
     sh.init<Pl, CG>();
     const int h = blockIdx.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -540,118 +653,150 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
     float4 *zf = reinterpret_cast<float4*>(ex + Pl::oZ) + lane, *df = reinterpret_cast<float4*>(ex + Pl::oD) + lane;
     Waits wait;
 
-    if (w < CG) {
-        const size_t sb = ((size_t)b * a.H + h) * DK * a.dv;
-        float S[DK / 8][4];
+    if (w < 2 * CG) {
+        constexpr int KH = KK / 2;
+        const int hf = w / CG, qa = hf, qb = 3 - hf;
+        const size_t sb = (((size_t)b * a.H + h) * DK + hf * (DK / 2)) * a.dv;
+        float S[DK / 16][4];
         read_state(S, dfinal ? dfinal + sb : nullptr, a.dv, col0 + g, t);
+        float m_own = tiles_max(S);
+        uint8_t *xf = ex + Pl::oX, *ef = ex + Pl::oE;
+        // R of quarter q, in its owner's part of the exchange of X: quarters 0, 3, 1, 2
+        auto rf = [&](int q) { return xf + (q == 0 ? 0 : q == 3 ? 1024 : q == 1 ? 2048 : 3072); };
         for (int it = 0; it < n_chunks; it++) {
-            uint8_t* st = sh.sm + (it % NS) * Pl::stage;
+            uint8_t* st = sh.sm + (it % NA) * Pl::A;
             const uint32_t sK = tc::smem_u32(st), sT = sK + Pl::oT;
-            const float* gt = reinterpret_cast<const float*>(st + Pl::oGate);
+            const float* gt = reinterpret_cast<const float*>(st + Pl::aGate);
 
-            // dS^T K^T
-            float inv;
-            const float ss = tiles_scale(S, inv);
-            const float si = inv;
-            float U[8][4];
-            zero(U);
-            wait(sh.full + it % NS, it / NS);
+            // the half's dS^T K^T
+            float si;
+            const float ss = scale_for(m_own, si);
+            float X[8][4];
+            zero(X);
+            wait(sh.fa + it % NA, it / NA);
             if (it > 0) wait(sh.s_free + cg, it - 1);
 #pragma unroll
-            for (int kk = 0; kk < KK; kk++) {
+            for (int kk = 0; kk < KH; kk++) {
                 uint32_t hi[4], lo[4];
                 split_a(S[2 * kk], S[2 * kk + 1], ss, hi, lo);
-                put4(sf + kk * 512, hi, lane);
-                put4(sf + Pl::sHalf + kk * 512, lo, lane);
+                put4(sf + (hf * KH + kk) * 512, hi, lane);
+                put4(sf + Pl::sHalf + (hf * KH + kk) * 512, lo, lane);
                 uint32_t bk[4][4];
 #pragma unroll
-                for (int p = 0; p < 4; p++) ldsm4(bk[p], at_n(sK, 16 * p, 2 * kk, lane));
-                mma_row<0, 4>(U, hi, bk);
-                mma_row<0, 4>(U, lo, bk);
+                for (int p = 0; p < 4; p++) ldsm4(bk[p], at_n(sK, 16 * p, 2 * (hf * KH + kk), lane));
+                mma_row<0, 4>(X, hi, bk);
+                mma_row<0, 4>(X, lo, bk);
             }
-            if (lane == 0) sh.s_inv[cg] = si;
+            if (lane == 0) {
+                sh.s_inv[2 * cg + hf] = si;
+                sh.s_max[2 * cg + hf] = m_own;
+            }
             signal(sh.s_ready + cg, lane);
-            scale_tokens(U, gt + gEC, si, t);
+            float U[4][4];
+            hand_over(xf, X, hf, si, lane, U);
             wait(sh.z_ready + cg, it);
+            tc::barrier(1 + cg, 64);
+            take_over(xf, hf, lane, U);
+            const float bound = fmaxf(sh.v_max[2 * cg], fmaxf(sh.s_max[2 * cg], sh.s_max[2 * cg + 1])) *
+                                fmaxf(1.f, fmaxf(gt[gMax], gt[gMax + 1]));
+            float ui;
+            const float us = bound_scale(bound, ui);
 #pragma unroll
-            for (int n = 0; n < 8; n++) {
-                const float4 d = df[32 * n];
-                U[n][0] += d.x, U[n][1] += d.y, U[n][2] += d.z, U[n][3] += d.w;
+            for (int n = 0; n < 4; n++) {
+                const int tile = 2 * (n < 2 ? qa : qb) + (n & 1);
+                const float2 e2 = *reinterpret_cast<const float2*>(gt + gEC + 8 * tile + 2 * t);
+                const float4 d = df[32 * tile];
+                U[n][0] = fmaf(U[n][0], e2.x, d.x), U[n][1] = fmaf(U[n][1], e2.y, d.y);
+                U[n][2] = fmaf(U[n][2], e2.x, d.z), U[n][3] = fmaf(U[n][3], e2.y, d.w);
             }
-            const float us = tiles_scale(U, inv);
-            const float ui = inv;
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                uint32_t hi[4], lo[4];
+                const int q = i ? qb : qa;
+                split_a(U[2 * i], U[2 * i + 1], us, hi, lo);
+                put4(rf(q), hi, lane);
+                put4(rf(q) + 512, lo, lane);
+            }
+            tc::barrier(1 + cg, 64);
 
             // Y^T = dU^T T: token j takes i >= j
-            float Y[8][4];
+            float Y[4][4];
             zero(Y);
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                uint32_t uh[4], ul[4];
-                split_a(U[2 * i], U[2 * i + 1], us, uh, ul);
-                uint32_t th[4][4], tl[4][4];
+                if (i < qa) continue;
+                uint32_t uh[4], ul[4], th[2][4], tl[2][4];
+                get4(rf(i), uh, lane);
+                get4(rf(i) + 512, ul, lane);
 #pragma unroll
-                for (int d = 0; d <= i; d++) {
-                    ldsm4_t(th[d], at_k(sT, 16 * i, 2 * d, lane));
-                    ldsm4_t(tl[d], at_k(sT + kTile, 16 * i, 2 * d, lane));
-                }
-#pragma unroll
-                for (int k = 0; k < 3; k++)
-#pragma unroll
-                    for (int d = 0; d <= i; d++) {
-                        const uint32_t(&b)[4] = k == 2 ? tl[d] : th[d];
-                        mma(Y[2 * d], k == 1 ? ul : uh, b[0], b[1]);
-                        mma(Y[2 * d + 1], k == 1 ? ul : uh, b[2], b[3]);
+                for (int k = 0; k < 2; k++)
+                    if (!k || i >= qb) {
+                        ldsm4_t(th[k], at_k(sT, 16 * i, 2 * (k ? qb : qa), lane));
+                        ldsm4_t(tl[k], at_k(sT + kTile, 16 * i, 2 * (k ? qb : qa), lane));
                     }
+#pragma unroll
+                for (int m = 0; m < 3; m++)
+#pragma unroll
+                    for (int k = 0; k < 2; k++)
+                        if (!k || i >= qb) {
+                            const uint32_t(&x)[4] = m == 2 ? tl[k] : th[k];
+                            mma(Y[2 * k], m == 1 ? ul : uh, x[0], x[1]);
+                            mma(Y[2 * k + 1], m == 1 ? ul : uh, x[2], x[3]);
+                        }
             }
-            const float ys = tiles_scale(Y, inv);  // of us-scaled values
-            const float yi = inv * ui;
             if (it > 0) wait(sh.u_free + cg, it - 1);
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                uint32_t hi[4], lo[4];
+                const int q = i ? qb : qa;
+                float E[2][4];
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    const int at = 16 * q + 8 * k + 2 * t;
+                    const float2 eg = *reinterpret_cast<const float2*>(gt + gEG + at);
+                    const float2 bt = *reinterpret_cast<const float2*>(gt + gBeta + at);
+                    E[k][0] = -Y[2 * i + k][0] * (eg.x * bt.x), E[k][1] = -Y[2 * i + k][1] * (eg.y * bt.y);
+                    E[k][2] = -Y[2 * i + k][2] * (eg.x * bt.x), E[k][3] = -Y[2 * i + k][3] * (eg.y * bt.y);
+                }
+                split_a(E[0], E[1], 1.f, hi, lo);
+                put4(ef + q * 1024, hi, lane);
+                put4(ef + q * 1024 + 512, lo, lane);
+                split_a(Y[2 * i], Y[2 * i + 1], 1.f, hi, lo);
+                put4(uf + q * 512, hi, lane);
+                put4(uf + Pl::uHalf + q * 512, lo, lane);
+            }
+            if (lane == 0 && hf == 0) sh.u_inv[cg] = ui;
+            signal(sh.u_ready + cg, lane);
+            tc::barrier(1 + cg, 64);
+
+            // the half's dS^T <- exp(G_C) dS^T + Z - (exp(G) beta' Y)^T K
+            const float eC = gt[gEG + C - 1];
             uint32_t yh[4][4], yl[4][4];
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                split_a(Y[2 * j], Y[2 * j + 1], ys, yh[j], yl[j]);
-                put4(uf + j * 512, yh[j], lane);
-                put4(uf + Pl::uHalf + j * 512, yl[j], lane);
+                get4(ef + j * 1024, yh[j], lane);
+                get4(ef + j * 1024 + 512, yl[j], lane);
             }
-            if (lane == 0) sh.u_inv[cg] = yi;
-            signal(sh.u_ready + cg, lane);
-
-            // dS^T <- exp(G_C) dS^T + Z - (exp(G) beta' Y)^T K
-            const float eC = gt[gEG + C - 1];
-            scale_tokens(Y, gt + gEG, -ys, t);
-            scale_tokens(Y, gt + gBeta, 1.f, t);
+            float m[4] = {0.f, 0.f, 0.f, 0.f};
+            constexpr int D = KH < 4 ? KH : 4;
 #pragma unroll
-            for (int j = 0; j < 4; j++) split_a(Y[2 * j], Y[2 * j + 1], 1.f, yh[j], yl[j]);
-#pragma unroll
-            for (int d = 0; d < KK; d += 4) {
+            for (int d = 0; d < KH; d += D) {
                 float acc[8][4];
+                state_product<D>(acc, yh, yl, sK, hf * KH + d, lane);
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    uint32_t b[4][4];
+                for (int i = 0; i < 2 * D; i++) {
+                    const float4 z4 = zf[32 * (2 * (hf * KH + d) + i)];
+                    const float z[4] = {z4.x, z4.y, z4.z, z4.w};
 #pragma unroll
-                    for (int i = 0; i < 4; i++) ldsm4_t(b[i], at_k(sK, 16 * j, 2 * (d + i), lane));
-                    if (j == 0) {
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            mma0(acc[2 * i], yh[j], b[i][0], b[i][1]);
-                            mma0(acc[2 * i + 1], yh[j], b[i][2], b[i][3]);
-                        }
-                    } else {
-                        mma_row<0, 4>(acc, yh[j], b);
+                    for (int e = 0; e < 4; e++) {
+                        S[2 * d + i][e] = fmaf(ui, acc[i][e], fmaf(eC, S[2 * d + i][e], z[e]));
+                        m[e] = fmaxf(m[e], fabsf(S[2 * d + i][e]));
                     }
-                    mma_row<0, 4>(acc, yl[j], b);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const float4 z = zf[32 * (2 * d + i)];
-                    S[2 * d + i][0] = fmaf(yi, acc[i][0], fmaf(eC, S[2 * d + i][0], z.x));
-                    S[2 * d + i][1] = fmaf(yi, acc[i][1], fmaf(eC, S[2 * d + i][1], z.y));
-                    S[2 * d + i][2] = fmaf(yi, acc[i][2], fmaf(eC, S[2 * d + i][2], z.z));
-                    S[2 * d + i][3] = fmaf(yi, acc[i][3], fmaf(eC, S[2 * d + i][3], z.w));
                 }
             }
             signal(sh.z_free + cg, lane);
-            signal(sh.empty + it % NS, lane);
+            signal(sh.ea + it % NA, lane);
+            m_own = warp_max(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
         }
         if (dinitial) write_state(S, dinitial + sb, a.dv, col0 + g, t);
         return;
@@ -659,30 +804,35 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
 
     const int hk = h / (a.H / a.Hk);
     const size_t kc0 = ((size_t)b * a.Hk + hk) * a.nc;
-    const bool feeds = w == CG && lane == 0, keeps = col0 < a.dv;
-    auto load = [&](int it) {
-        const int c = n_chunks - 1 - it;
-        load_stage<Pl, DK>(sh, a, kc0 + c, ch0 + c, it, wait);
+    const bool feeds = w == 2 * CG && lane == 0, keeps = col0 < a.dv;
+    auto load = [&](int na, int nb) {
+        if (na < n_chunks) load_a<Pl, DK>(sh, a, kc0 + n_chunks - 1 - na, ch0 + n_chunks - 1 - na, na, wait);
+        if (nb < n_chunks) load_b<Pl, DK>(sh, a, kc0 + n_chunks - 1 - nb, ch0 + n_chunks - 1 - nb, nb, wait);
     };
-    if (feeds)
-        for (int it = 0; it < NS - 1 && it < n_chunks; it++) load(it);
+    if (feeds) {
+        for (int it = 0; it < NB - 1; it++) load(n_chunks, it);
+        for (int it = 0; it < NA - 1; it++) load(it, n_chunks);
+    }
     const Rows orows = rows_at(a.dout, a, b, h, col0 + 8 * (lane & 1), len);
     uint4 on[4];
     if (n_chunks)
 #pragma unroll
         for (int i = 0; i < 4; i++) on[i] = orows.load((n_chunks - 1) * C + 16 * i + (lane >> 1));
     for (int it = 0; it < n_chunks; it++) {
-        if (feeds && it + NS - 1 < n_chunks) load(it + NS - 1);
+        if (feeds) {  // the helper's own first: the chain's may wait for the chain
+            load(n_chunks, it + NB - 1);
+            load(it + NA - 1, n_chunks);
+        }
         __syncwarp();
         {  // dO' of this chunk: its record's tile, dU0 and Z
             const int c = n_chunks - 1 - it;
-            uint8_t* st = sh.sm + (it % NS) * Pl::stage;
-            const uint32_t sQ = tc::smem_u32(st) + 2 * C * DK, sP = tc::smem_u32(st) + Pl::oT + 2 * kTile;
-            const float* gt = reinterpret_cast<const float*>(st + Pl::oGate);
+            uint8_t* st = sh.sm + Pl::oB + (it % NB) * Pl::B;
+            const uint32_t sQ = tc::smem_u32(st), sP = sQ + Pl::oP;
+            const float* gt = reinterpret_cast<const float*>(st + Pl::bGate);
             uint8_t* rec = a.records + ((ch0 + c) * groups_of(a.dv) + group) * Record<DK>::bytes;
             float* rf = reinterpret_cast<float*>(rec + Record<DK>::f);
             float o[8][4];
-            wait(sh.full + it % NS, it / NS);
+            wait(sh.fb + it % NB, it / NB);
 #pragma unroll
             for (int p = 0; p < 4; p++) {
                 uint32_t v4[4];
@@ -725,6 +875,7 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
             scale_tokens(o, gt + gEG, os, t);
 #pragma unroll
             for (int i = 0; i < 4; i++) split_a(o[2 * i], o[2 * i + 1], 1.f, oh[i], ol[i]);
+            const float um = tiles_max(U) * oi;
             if (it > 0) wait(sh.z_free + cg, it - 1);
 #pragma unroll
             for (int n = 0; n < 8; n++) df[32 * n] = make_float4(U[n][0] * oi, U[n][1] * oi, U[n][2] * oi, U[n][3] * oi);
@@ -732,28 +883,14 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
 #pragma unroll 1
             for (int d = 0; d < KK; d += 4) {
                 float acc[8][4];
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    uint32_t b[4][4];
-#pragma unroll
-                    for (int i = 0; i < 4; i++) ldsm4_t(b[i], at_k(sQ, 16 * j, 2 * (d + i), lane));
-                    if (j == 0) {
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            mma0(acc[2 * i], oh[j], b[i][0], b[i][1]);
-                            mma0(acc[2 * i + 1], oh[j], b[i][2], b[i][3]);
-                        }
-                    } else {
-                        mma_row<0, 4>(acc, oh[j], b);
-                    }
-                    mma_row<0, 4>(acc, ol[j], b);
-                }
+                state_product<4>(acc, oh, ol, sQ, d, lane);
 #pragma unroll
                 for (int i = 0; i < 8; i++)
                     zf[32 * (2 * d + i)] = make_float4(acc[i][0] * oi, acc[i][1] * oi, acc[i][2] * oi, acc[i][3] * oi);
             }
+            if (lane == 0) sh.v_max[2 * cg] = um;
             signal(sh.z_ready + cg, lane);
-            signal(sh.empty + it % NS, lane);
+            signal(sh.eb + it % NB, lane);
         }
         {  // the chain's tiles of this chunk into its record
             uint8_t* rec = a.records + ((ch0 + n_chunks - 1 - it) * groups_of(a.dv) + group) * Record<DK>::bytes;
@@ -768,7 +905,7 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
                     get4(sf + Pl::sHalf + kk * 512, r, lane);
                     keep_tile(rec + Record<DK>::ds + 32 * DK, 2 * kk, lane, r);
                 }
-                if (lane == 0) rf[fDs] = sh.s_inv[cg];
+                if (lane < 2) rf[fDs + lane] = sh.s_inv[2 * cg + lane];
             }
             signal(sh.s_free + cg, lane);
             wait(sh.u_ready + cg, it);

@@ -124,6 +124,8 @@ __global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, Tables tb,
         gt[gSq + tid] = sq[tid];
         reinterpret_cast<double*>(gt + kGates / 4)[tid] = sG[tid];
         sb[tid] = bh;  // read by others after the next barrier
+        const float m = warp_max(fabsf(bh));
+        if (lane == 0) gt[gMax + w] = m;
     }
 
     // scores
