@@ -51,7 +51,8 @@ enum : int { kOutBf16 = 0, kOutF32 = 1, kKeep = 2, kBack = 3 };
 // Shared memory of a block of CG groups of 16 columns.
 template <int DK, int CG, int MODE>
 struct Plan {
-    static constexpr int warps = 3 * CG;  // 2 CG of the chains, then CG helpers
+    // 2 CG warps of the chains, CG helpers, and CG that write the records
+    static constexpr int warps = MODE == kKeep || MODE == kBack ? 4 * CG : 3 * CG;
     // Two rings: the chain warps' K', T and gates, and the helpers' Q', P and gates.
     static constexpr int kGateRoom = 1536, keys = 2 * C * DK;
     static constexpr int oT = keys, aGate = oT + 2 * kTile, A = aGate + kGateRoom;
@@ -499,6 +500,7 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
             if (na < n_chunks) load_a<Pl, DK>(sh, a, kc0 + na, ch0 + na, na, wait);
         }
         __syncwarp();
+        if (MODE == kKeep && w < 3 * CG) continue;  // only feeds
         if constexpr (MODE == kKeep) {
             // the operand tiles into the chunk's record
             uint8_t* rec = a.records + ((ch0 + c) * groups_of(a.dv) + group) * Record<DK>::bytes;
@@ -802,9 +804,43 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
         return;
     }
 
+    const bool keeps = col0 < a.dv;
+    if (w >= 3 * CG) {  // the chain's tiles of every chunk into its record
+        for (int it = 0; it < n_chunks; it++) {
+            uint8_t* rec = a.records + ((ch0 + n_chunks - 1 - it) * groups_of(a.dv) + group) * Record<DK>::bytes;
+            float* rf = reinterpret_cast<float*>(rec + Record<DK>::f);
+            wait(sh.s_ready + cg, it);
+            if (keeps) {
+#pragma unroll 4
+                for (int kk = 0; kk < KK; kk++) {
+                    uint32_t r[4];
+                    get4(sf + kk * 512, r, lane);
+                    keep_tile(rec + Record<DK>::ds, 2 * kk, lane, r);
+                    get4(sf + Pl::sHalf + kk * 512, r, lane);
+                    keep_tile(rec + Record<DK>::ds + 32 * DK, 2 * kk, lane, r);
+                }
+                if (lane < 2) rf[fDs + lane] = sh.s_inv[2 * cg + lane];
+            }
+            signal(sh.s_free + cg, lane);
+            wait(sh.u_ready + cg, it);
+            if (keeps) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    uint32_t r[4];
+                    get4(uf + j * 512, r, lane);
+                    keep_tile(rec + Record<DK>::y, 2 * j, lane, r);
+                    get4(uf + Pl::uHalf + j * 512, r, lane);
+                    keep_tile(rec + Record<DK>::y + 2048, 2 * j, lane, r);
+                }
+                if (lane == 0) rf[fY] = sh.u_inv[cg];
+            }
+            signal(sh.u_free + cg, lane);
+        }
+        return;
+    }
     const int hk = h / (a.H / a.Hk);
     const size_t kc0 = ((size_t)b * a.Hk + hk) * a.nc;
-    const bool feeds = w == 2 * CG && lane == 0, keeps = col0 < a.dv;
+    const bool feeds = w == 2 * CG && lane == 0;
     auto load = [&](int na, int nb) {
         if (na < n_chunks) load_a<Pl, DK>(sh, a, kc0 + n_chunks - 1 - na, ch0 + n_chunks - 1 - na, na, wait);
         if (nb < n_chunks) load_b<Pl, DK>(sh, a, kc0 + n_chunks - 1 - nb, ch0 + n_chunks - 1 - nb, nb, wait);
@@ -891,36 +927,6 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
             if (lane == 0) sh.v_max[2 * cg] = um;
             signal(sh.z_ready + cg, lane);
             signal(sh.eb + it % NB, lane);
-        }
-        {  // the chain's tiles of this chunk into its record
-            uint8_t* rec = a.records + ((ch0 + n_chunks - 1 - it) * groups_of(a.dv) + group) * Record<DK>::bytes;
-            float* rf = reinterpret_cast<float*>(rec + Record<DK>::f);
-            wait(sh.s_ready + cg, it);
-            if (keeps) {
-#pragma unroll 4
-                for (int kk = 0; kk < KK; kk++) {
-                    uint32_t r[4];
-                    get4(sf + kk * 512, r, lane);
-                    keep_tile(rec + Record<DK>::ds, 2 * kk, lane, r);
-                    get4(sf + Pl::sHalf + kk * 512, r, lane);
-                    keep_tile(rec + Record<DK>::ds + 32 * DK, 2 * kk, lane, r);
-                }
-                if (lane < 2) rf[fDs + lane] = sh.s_inv[2 * cg + lane];
-            }
-            signal(sh.s_free + cg, lane);
-            wait(sh.u_ready + cg, it);
-            if (keeps) {
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    uint32_t r[4];
-                    get4(uf + j * 512, r, lane);
-                    keep_tile(rec + Record<DK>::y, 2 * j, lane, r);
-                    get4(uf + Pl::uHalf + j * 512, r, lane);
-                    keep_tile(rec + Record<DK>::y + 2048, 2 * j, lane, r);
-                }
-                if (lane == 0) rf[fY] = sh.u_inv[cg];
-            }
-            signal(sh.u_free + cg, lane);
         }
     }
 }
