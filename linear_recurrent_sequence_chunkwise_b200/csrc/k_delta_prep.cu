@@ -51,7 +51,7 @@ __device__ __forceinline__ int row_exponent(const float (&x)[8]) {
 }
 
 template <int DK>
-__global__ void __launch_bounds__(kThreads) k_delta_prep(DeltaArgs a, Tables tb, int nc) {
+__global__ void __launch_bounds__(kThreads, DK == 256 ? 3 : 4) k_delta_prep(DeltaArgs a, Tables tb, int nc) {
     using Sm = Smem<DK>;
     extern __shared__ __align__(1024) uint8_t sm[];
     __shared__ double sG[C];

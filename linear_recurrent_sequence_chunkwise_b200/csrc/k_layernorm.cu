@@ -407,14 +407,13 @@ bool wide_rows(const LayerNormArgs& a) {
 template <typename T, typename W, int VEC, int ELEMS>
 ret_status fwd_go(const LayerNormArgs& a, cudaStream_t s) {
     const int group = group_for(a.d, ELEMS), threads = group == 32 ? 128 : group, ng = threads / group;
-    const long long fit = kSms * (ELEMS > 16 ? 640 : 768) / threads;  // what the registers let an SM hold
+    const long long fit = kSms * 1024 / threads;  // what the registers let an SM hold
     const unsigned blocks = (unsigned)std::min<long long>(fit, (a.rows + ng - 1) / ng);
     auto go = [&](auto kern) {
         kern<<<blocks, threads, 0, s>>>((const T*)a.x, (const W*)a.gain, (const W*)a.bias, (T*)a.y, a.mean, a.rstd, a.rows,
                                         a.d, (float)a.eps, group);
         return check_launch("ret_layernorm_forward");
     };
-    if constexpr (ELEMS == 32) return go(k_ln_forward<T, W, VEC, ELEMS / VEC, true>);
     if constexpr (VEC > 1)
         if (a.d == group * ELEMS && a.gain && a.bias) return go(k_ln_forward<T, W, VEC, ELEMS / VEC, true>);
     return go(k_ln_forward<T, W, VEC, ELEMS / VEC, false>);
@@ -423,11 +422,6 @@ template <typename T, typename W>
 ret_status fwd(const LayerNormArgs& a, cudaStream_t s) {
     constexpr int V = 16 / (int)sizeof(T);
     if (!wide_rows(a)) return fwd_go<T, W, 1, 16>(a, s);
-    // A lane takes 32 bf16 elements when two warps of them hold the row exactly
-    // and there are rows for every group; few rows finish sooner with more
-    // threads each, and 32 in fp32 do not fit the registers.
-    if constexpr (V == 8)
-        if (a.rows > kSms && a.d > 512 && a.gain && a.bias && a.d == group_for(a.d, 32) * 32) return fwd_go<T, W, V, 32>(a, s);
     return fwd_go<T, W, V, 16>(a, s);
 }
 
