@@ -833,6 +833,11 @@ def ret_delta_forward_chunkwise(q, k, v, g, beta, lengths=None, initial_state=No
     the device or None, states [B, H, dk, dv] fp32.  Returns ``out`` [B, N, H, dv]
     (rows behind a sequence's end are not written), or ``(out, final_state)``
     when a final state is requested (passed in or ``want_final_state``)."""
+    if final_state is workspace is stream is None and (out_dtype is None or out_dtype in FLOATS):
+        r = _binding.delta_forward(q, k, v, g, beta, lengths, initial_state, out,
+                                   (out_dtype or q.dtype) is torch.bfloat16, want_final_state)
+        if r is not None:
+            return r
     (B, N), Hk, H, dk, dv = _delta_shapes(q, k, v, g, beta, 2)
     _seq_outputs(q, out, final_state, B, N, H, dk, dv, initial_state)
     _buf(lengths, "lengths", (B,), (torch.int32,), q)
@@ -883,6 +888,11 @@ def ret_delta_backward_chunkwise(q, k, v, g, beta, dout, lengths=None, initial_s
     dinitial_state); dq, dk, dv of ``grad_dtype``, the others fp32.
     dinitial_state is None unless an initial state is given, it is passed in
     or wanted."""
+    if dq is dk is dv is dg is dbeta is dinitial_state is workspace is stream is None and grad_dtype in FLOATS:
+        r = _binding.delta_backward(q, k, v, g, beta, lengths, initial_state, dout, dfinal_state, grad_dtype is torch.bfloat16,
+                                    initial_state is not None if want_dinitial_state is None else want_dinitial_state)
+        if r is not None:
+            return r
     (B, N), Hk, H, dk_, dv_ = _delta_shapes(q, k, v, g, beta, 2)
     _buf(dout, "dout", (B, N, H, dv_), (q.dtype,), q)
     _buf(initial_state, "initial_state", (B, H, dk_, dv_), F32, q)

@@ -46,12 +46,41 @@ int device_of(const Tensor& t) {
 }
 
 PyObject* pass() { Py_RETURN_NONE; }
+// A tuple of tensors, None for an undefined one.
 PyObject* tuple(std::initializer_list<Tensor> ts) {
     PyObject* r = PyTuple_New((Py_ssize_t)ts.size());
     Py_ssize_t i = 0;
-    for (const Tensor& t : ts) PyTuple_SET_ITEM(r, i++, THPVariable_Wrap(t));
+    for (const Tensor& t : ts) PyTuple_SET_ITEM(r, i++, t.defined() ? THPVariable_Wrap(t) : pass());
     return r;
 }
+const float* fptr(const Tensor* t) { return t ? t->data_ptr<float>() : nullptr; }
+
+// q, k, v, g, beta, lengths, initial_state of a call over sequences.
+struct Delta {
+    const Tensor *q, *k, *v, *g, *beta, *lengths, *state;
+    int dev, B, N, Hk, H, dk, dv;
+    bool read(PyObject* const* a) {
+        const Tensor** t[] = {&q, &k, &v, &g, &beta};
+        for (int i = 0; i < 5; i++)
+            if (!(*t[i] = tensor(a[i]))) return false;
+        lengths = a[5] == Py_None ? nullptr : tensor(a[5]);
+        state = a[6] == Py_None ? nullptr : tensor(a[6]);
+        if ((a[5] != Py_None && !lengths) || (a[6] != Py_None && !state)) return false;
+        dev = device_of(*q);
+        if (dev < 0 || !is_float(*q) || q->dim() != 4 || v->dim() != 4 || k->sizes() != q->sizes() || v->size(0) != q->size(0) ||
+            v->size(1) != q->size(1))
+            return false;
+        for (const Tensor* x : {q, k, v})
+            if (!plain(*x, dev) || x->scalar_type() != q->scalar_type()) return false;
+        for (int64_t x : {q->size(0), q->size(1), q->size(2), q->size(3), v->size(2), v->size(3)})
+            if (x < 1 || x > INT32_MAX) return false;
+        B = (int)q->size(0), N = (int)q->size(1), Hk = (int)q->size(2), dk = (int)q->size(3);
+        H = (int)v->size(2), dv = (int)v->size(3);
+        return f32(*g, dev, {B, N, H}) && f32(*beta, dev, {B, N, H}) && (!state || f32(*state, dev, {B, H, dk, dv})) &&
+               (!lengths || (lengths->scalar_type() == at::kInt && plain(*lengths, dev) && lengths->sizes() == at::IntArrayRef({B})));
+    }
+    const int32_t* lens() const { return lengths ? lengths->data_ptr<int32_t>() : nullptr; }
+};
 // Runs f; a C++ exception (no memory, say) becomes None, and the general way meets it again.
 template <typename F>
 PyObject* guarded(F f) {
@@ -146,6 +175,57 @@ PyObject* delta_decode_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// (q, k, v, g, beta, lengths, initial_state, out, out in bf16, want_final_state)
+PyObject* delta_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Delta d;
+        if (n != 10 || !d.read(a)) return pass();
+        Tensor out, final_state, ws;
+        if (a[7] == Py_None) {
+            out = make({d.B, d.N, d.H, d.dv}, PyObject_IsTrue(a[8]) == 1 ? at::kBFloat16 : at::kFloat, d.dev);
+        } else {
+            const Tensor* o = tensor(a[7]);
+            if (!o || !is_float(*o) || !plain(*o, d.dev) || o->sizes() != d.v->sizes()) return pass();
+            out = *o;
+        }
+        if (PyObject_IsTrue(a[9]) == 1) final_state = make({d.B, d.H, d.dk, d.dv}, at::kFloat, d.dev);
+        const size_t need = ret_delta_workspace_bytes(d.B, d.N, d.Hk, d.H, d.dk, d.dv, code(*d.q));
+        if (need) ws = make({(int64_t)need}, at::kByte, d.dev);
+        if (ret_delta_forward_chunkwise(d.q->data_ptr(), d.k->data_ptr(), d.v->data_ptr(), fptr(d.g), fptr(d.beta), d.lens(),
+                                        fptr(d.state), d.B, d.N, d.Hk, d.H, d.dk, d.dv, out.data_ptr(),
+                                        final_state.defined() ? final_state.data_ptr<float>() : nullptr, stream(d.dev),
+                                        code(*d.q), code(out), need ? ws.data_ptr() : nullptr, need) != RET_OK)
+            return pass();
+        return final_state.defined() ? tuple({out, final_state}) : THPVariable_Wrap(out);
+    });
+}
+
+// (q, k, v, g, beta, lengths, initial_state, dout, dfinal_state, gradients in bf16, want_dinitial_state)
+PyObject* delta_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Delta d;
+        if (n != 11 || !d.read(a)) return pass();
+        const Tensor *dout = tensor(a[7]), *dfinal = a[8] == Py_None ? nullptr : tensor(a[8]);
+        if (!dout || dout->scalar_type() != d.q->scalar_type() || !plain(*dout, d.dev) || dout->sizes() != d.v->sizes() ||
+            (a[8] != Py_None && (!dfinal || !f32(*dfinal, d.dev, {d.B, d.H, d.dk, d.dv}))))
+            return pass();
+        const size_t need = ret_delta_backward_workspace_bytes(d.B, d.N, d.Hk, d.H, d.dk, d.dv, code(*d.q));
+        if (!need) return pass();
+        const at::ScalarType type = PyObject_IsTrue(a[9]) == 1 ? at::kBFloat16 : at::kFloat;
+        Tensor dq = make(d.q->sizes(), type, d.dev), dk = make(d.k->sizes(), type, d.dev), dv = make(d.v->sizes(), type, d.dev);
+        Tensor dg = make(d.g->sizes(), at::kFloat, d.dev), dbeta = make(d.g->sizes(), at::kFloat, d.dev), ds0;
+        if (PyObject_IsTrue(a[10]) == 1) ds0 = make({d.B, d.H, d.dk, d.dv}, at::kFloat, d.dev);
+        Tensor ws = make({(int64_t)need}, at::kByte, d.dev);
+        if (ret_delta_backward_chunkwise(d.q->data_ptr(), d.k->data_ptr(), d.v->data_ptr(), fptr(d.g), fptr(d.beta),
+                                         dout->data_ptr(), d.lens(), fptr(d.state), fptr(dfinal), d.B, d.N, d.Hk, d.H, d.dk, d.dv,
+                                         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr<float>(),
+                                         dbeta.data_ptr<float>(), ds0.defined() ? ds0.data_ptr<float>() : nullptr, stream(d.dev),
+                                         code(*d.q), code(dq), ws.data_ptr(), need) != RET_OK)
+            return pass();
+        return tuple({dq, dk, dv, dg, dbeta, ds0});
+    });
+}
+
 // (q, k, freqs, positions, pos_offset, half, scale, inverse)
 PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
@@ -180,6 +260,8 @@ PyMethodDef methods[] = {
     {"layernorm_forward", (PyCFunction)(void*)layernorm_forward, METH_FASTCALL, nullptr},
     {"layernorm_backward", (PyCFunction)(void*)layernorm_backward, METH_FASTCALL, nullptr},
     {"delta_decode_step", (PyCFunction)(void*)delta_decode_step, METH_FASTCALL, nullptr},
+    {"delta_forward", (PyCFunction)(void*)delta_forward, METH_FASTCALL, nullptr},
+    {"delta_backward", (PyCFunction)(void*)delta_backward, METH_FASTCALL, nullptr},
     {"rotary", (PyCFunction)(void*)rotary, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
