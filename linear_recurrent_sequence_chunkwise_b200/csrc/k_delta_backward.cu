@@ -19,7 +19,8 @@
 // A key head's gradient is the sum over its value heads: one block takes them
 // all, one after the other, so the order is fixed.  Sixteen warps: a row group
 // of 16 tokens and a quarter of dk each.  The records of 16 value columns come
-// through a ring of bulk copies that runs on across value heads,
+// through a ring of bulk copies that runs on across value heads and chunks (one
+// block an SM, each walking its share of the chunks),
 // and the five products over dv accumulate in registers; then the 64 x 64
 // scores go through shared memory once, in two terms, to meet K and Q.
 //
@@ -48,11 +49,11 @@ namespace {
 struct GradArgs {
     Tables tb;
     const int* lengths;
-    const __nv_bfloat16* v;
     const uint8_t* records;
+    float4* sums;  // more than one value head to a key head: its gradients so far
     void *dq, *dk, *dv;
     float *dg, *dbeta;
-    int N, nc, Hk, H, dv_dim;
+    int N, nc, Hk, H, dv_dim, B;
 };
 
 template <int DK>
@@ -63,11 +64,10 @@ struct Grad {
     static constexpr int oK = 0, oQ = 2 * C * DK;      // K, Q
     static constexpr int oE = 4 * C * DK;              // E D, W D, beta W D: hi, lo each
     static constexpr int oR = oE + 6 * kTile;          // the ring
-    static constexpr int most = 222 * 1024;
-    static constexpr int fit = (most - oR - 2 * 2048) / Record<DK>::bytes;
-    static constexpr int stages = fit > 6 ? 6 : fit;
-    static constexpr int oG = oR + stages * Record<DK>::bytes;  // the gates of this value head and the next one
-    static constexpr int smem = oG + 2 * 2048 + 1024;
+    // a stage: a record, 16 columns of V, the head's gates
+    static constexpr int oV = Record<DK>::bytes, oGate = oV + C * 32, stage = (oGate + kGateRow + 127) / 128 * 128;
+    static constexpr int most = 222 * 1024, fit = (most - oR) / stage, stages = fit > 6 ? 6 : fit;
+    static constexpr int smem = oR + stages * stage + 1024;
 };
 
 template <typename T>
@@ -80,26 +80,108 @@ __device__ __forceinline__ float2 sum_h2(uint32_t hi, uint32_t lo) {
     return make_float2(h.x + l.x, h.y + l.y);
 }
 
+// Accumulators in units of p, to be added to in units of q: a change of units is
+// exact (powers of two).  False if what is to be added lies more than 2^60 below
+// them, where it changes nothing and the new units would not hold them.
+template <int N>
+__device__ __forceinline__ bool in_units(float (&acc)[N][4], float& p, float q) {
+    if (p == q) return true;
+    const float f = p / q;
+    if (!(f <= 1.1529215e18f)) return false;
+#pragma unroll
+    for (int n = 0; n < N; n++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) acc[n][e] *= f;
+    p = q;
+    return true;
+}
+template <int N>
+__device__ __forceinline__ void times(float (&acc)[N][4], float f0, float f1) {
+#pragma unroll
+    for (int n = 0; n < N; n++) acc[n][0] *= f0, acc[n][1] *= f0, acc[n][2] *= f1, acc[n][3] *= f1;
+}
+
 template <int DK, typename T>
-__global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __grid_constant__ GradArgs a) {
+__global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __grid_constant__ CUtensorMap mv,
+                                                                          const __grid_constant__ GradArgs a) {
     using Gr = Grad<DK>;
     using Rec = Record<DK>;
     constexpr int NH = Gr::NH, DW = Gr::DW, NS = Gr::stages;
     extern __shared__ uint8_t raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    __shared__ uint64_t full[NS], empty[NS], keys, gfull[2], gempty[2];
+    __shared__ uint64_t full[NS], empty[NS], keys;
     __shared__ float inv_e[4][4], inv_w[4][4], inv_b[4][4];
     __shared__ float row_a[NH][C], row_c[NH][C], row_b[NH][C], red[Gr::warps];
-    const int c = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int rep = a.H / a.Hk, ng = groups_of(a.dv_dim);
-    const int L = min(C, length_of(a.lengths, b, a.N) - c * C);
-    const int rows = min(C, a.N - c * C);  // rows of the tensors in this chunk
-    const size_t row0 = (size_t)b * a.N + (size_t)c * C;
     T* dq = reinterpret_cast<T*>(a.dq);
     T* dk = reinterpret_cast<T*>(a.dk);
     T* dv = reinterpret_cast<T*>(a.dv);
+    // Items: (chunk, key head, sequence).  A block takes every gridDim.x-th, and
+    // its ring runs on from one to the next.
+    const int items = a.nc * a.Hk * a.B;
+    auto tokens_of = [&](int item) {
+        return min(C, length_of(a.lengths, item / (a.nc * a.Hk), a.N) - item % a.nc * C);
+    };
+    if (tid == 0) {
+        for (int i = 0; i < NS; i++) tc::mbar_init(full + i, 1), tc::mbar_init(empty + i, Gr::warps);
+        tc::mbar_init(&keys, 1);
+        tc::fence_barrier_init();
+    }
+    __syncthreads();
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int phase) {  // after one gave up the others are skipped: the barriers stay complete
+        if (ok && !tc::mbar_wait(bar, phase & 1)) {
+            ok = false;
+            atomicExch(&g_grad_err, kErrTimeout);
+        }
+    };
+    // One lane: the next record, its columns of V and its head's gates into the
+    // ring, ahead of the warps.
+    int ahead = blockIdx.x, stage = 0, round = 0, group = 0, head = 0, row = 0, seq = 0;
+    size_t chunk = 0;
+    auto find = [&]() {  // the next item with tokens
+        while (ahead < items && tokens_of(ahead) <= 0) ahead += gridDim.x;
+        if (ahead >= items) return;
+        const int c = ahead % a.nc, x = ahead / a.nc;
+        seq = x / a.Hk, head = x % a.Hk * rep, row = c * C;
+        chunk = ((size_t)seq * a.H + head) * a.nc + c;
+    };
+    auto load = [&]() {
+        if (ahead >= items) return;
+        uint64_t* bar = full + stage;
+        if (round > 0) wait(empty + stage, round - 1);
+        if (ok) {
+            uint8_t* st = sm + Gr::oR + stage * Gr::stage;
+            tc::mbar_arrive_expect_tx(bar, Rec::bytes + C * 32 + kGateRow);
+            bulk_load(st, a.records + (chunk * ng + group) * Rec::bytes, Rec::bytes, bar);
+            bulk_load(st + Gr::oGate, a.tb.gates + chunk * kGateRow, kGateRow, bar);
+            tc::tma_load_4d(st + Gr::oV, &mv, bar, 16 * group, head, row, seq);
+        }
+        if (++stage == NS) stage = 0, round++;
+        if (++group < ng) return;
+        group = 0, head++, chunk += a.nc;
+        if (head % rep == 0) {
+            ahead += gridDim.x;
+            find();
+        }
+    };
+    if (tid == 0) find();
+    if (tid == 0)
+        for (int i = 0; i < NS - 1; i++) load();
+    __syncwarp();
 
+    const int rg = w & 3, cg = w >> 2;  // row group, column share
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t base = tc::smem_u32(sm), sK = base + Gr::oK, sQ = base + Gr::oQ, sE = base + Gr::oE;
+    const int i0 = 16 * rg + g, i1 = i0 + 8;
+    int it = 0, done = 0;  // steps and items so far
+
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int c = item % a.nc, hk = item / a.nc % a.Hk, b = item / (a.nc * a.Hk);
+    const int L = tokens_of(item);
+    const int rows = min(C, a.N - c * C);  // rows of the tensors in this chunk
+    const size_t row0 = (size_t)b * a.N + (size_t)c * C;
     if (L <= 0) {  // behind the end: no gradient
         for (int i = tid; i < rows * DK; i += Gr::threads) {
             const size_t e = ((row0 + i / DK) * a.Hk + hk) * DK + i % DK;
@@ -115,66 +197,18 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
             a.dg[e] = 0.f;
             a.dbeta[e] = 0.f;
         }
-        return;
+        continue;
     }
-    if (tid == 0) {
-        for (int i = 0; i < NS; i++) tc::mbar_init(full + i, 1), tc::mbar_init(empty + i, Gr::warps);
-        for (int i = 0; i < 2; i++) tc::mbar_init(gfull + i, 1), tc::mbar_init(gempty + i, Gr::warps);
-        tc::mbar_init(&keys, 1);
-        tc::fence_barrier_init();
-    }
-    __syncthreads();
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, int phase) {  // after one gave up the others are skipped: the barriers stay complete
-        if (ok && !tc::mbar_wait(bar, phase & 1)) {
-            ok = false;
-            atomicExch(&g_grad_err, kErrTimeout);
-        }
-    };
-
-    // one lane: records and gates into the ring, ahead of the warps
-    const size_t ch0 = ((size_t)b * a.H + hk * rep) * a.nc + c;
-    const int steps = rep * ng;
-    auto load = [&](int s) {
-        if (s >= NS) wait(empty + s % NS, s / NS - 1);
-        if (!ok) return;
-        const int r = s / ng;
-        tc::mbar_arrive_expect_tx(full + s % NS, Rec::bytes);
-        bulk_load(sm + Gr::oR + (s % NS) * Rec::bytes, a.records + ((ch0 + (size_t)r * a.nc) * ng + s % ng) * Rec::bytes,
-                  Rec::bytes, full + s % NS);
-    };
-    auto load_gates = [&](int r) {
-        if (r >= 2) wait(gempty + (r & 1), (r >> 1) - 1);
-        if (!ok) return;
-        tc::mbar_arrive_expect_tx(gfull + (r & 1), kGateRow);
-        bulk_load(sm + Gr::oG + (r & 1) * 2048, a.tb.gates + (ch0 + (size_t)r * a.nc) * kGateRow, kGateRow, gfull + (r & 1));
-    };
-    if (tid == 0) {
-        load_gates(0);
-        for (int s = 0; s < NS - 1 && s < steps; s++) load(s);
+    if (tid == 0 && ok) {  // K and Q: the last item's readers have passed its last barrier
         tc::mbar_arrive_expect_tx(&keys, 4 * C * DK);
         bulk_load(sm, a.tb.keys + (((size_t)b * a.Hk + hk) * a.nc + c) * (4 * C * DK), 4 * C * DK, &keys);
     }
     __syncwarp();
+    float ik0 = 0.f, ik1 = 0.f, sq0 = 0.f, sq1 = 0.f;  // 1 / s_k and s_q of rows i0 and i1
 
-    const int rg = w & 3, cg = w >> 2;  // row group, column share
-    const int g = lane >> 2, t = lane & 3;
-    const uint32_t base = tc::smem_u32(sm), sK = base + Gr::oK, sQ = base + Gr::oQ, sE = base + Gr::oE;
-    const int i0 = 16 * rg + g, i1 = i0 + 8;
-
-    float dqa[DW / 8][4], dka[DW / 8][4];  // sums over the value heads
-#pragma unroll
-    for (int n = 0; n < DW / 8; n++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) dqa[n][e] = dka[n][e] = 0.f;
-
-    for (int r = 0, it = 0; r < rep; r++) {
+    for (int r = 0; r < rep; r++) {
         const int h = hk * rep + r;
-        const float* gt = reinterpret_cast<const float*>(sm + Gr::oG + (r & 1) * 2048);
-        const double* G = reinterpret_cast<const double*>(sm + Gr::oG + (r & 1) * 2048 + kGates);
-        if (tid == 0 && r + 1 < rep) load_gates(r + 1);
-        __syncwarp();
-        wait(gfull + (r & 1), r >> 1);
+        const float* gt = nullptr;
         float E[2][4], W[2][4], Zq[DW / 8][4], Z[DW / 8][4], Zw[DW / 8][4];
 #pragma unroll
         for (int n = 0; n < 2; n++)
@@ -186,27 +220,22 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
             for (int e = 0; e < 4; e++) Zq[n][e] = Z[n][e] = Zw[n][e] = 0.f;
         float db0 = 0.f, db1 = 0.f;  // Y . v of rows g and g + 8
         float inner = 0.f;           // <dS1, S0>
-        const float b0 = gt[gBeta + i0], b1 = gt[gBeta + i1], k0 = gt[gIk + i0], k1 = gt[gIk + i1];
+        float b0 = 0.f, b1 = 0.f;
+        float pe = 0.f, pw = 0.f, pq = 0.f, pz = 0.f, pu = 0.f;  // units of E, W, Zq, Z, Zw
 
         for (int gr = 0; gr < ng; gr++, it++) {
             const int st = it % NS;
-            if (tid == 0 && it + NS - 1 < steps) load(it + NS - 1);
+            if (tid == 0) load();
             __syncwarp();
-            const uint8_t* rec = sm + Gr::oR + st * Rec::bytes;
+            const uint8_t* rec = sm + Gr::oR + st * Gr::stage;
             const uint32_t sr = tc::smem_u32(rec);
             const float* f = reinterpret_cast<const float*>(rec + Rec::f);
-            // dv and Y . v: of the rows' 16 columns a share takes every fourth group
-            const bool mine = (gr & 3) == cg;
-            uint32_t v2[4] = {0, 0, 0, 0};
-            if (mine) {
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int row = 16 * rg + g + 8 * (e & 1), col = 16 * gr + 2 * t + 8 * (e >> 1);
-                    if (row < L && col < a.dv_dim)
-                        v2[e] = *reinterpret_cast<const uint32_t*>(a.v + ((row0 + row) * a.H + h) * a.dv_dim + col);
-                }
-            }
             wait(full + st, it / NS);
+            gt = reinterpret_cast<const float*>(rec + Gr::oGate);
+            if (gr == 0) {
+                b0 = gt[gBeta + i0], b1 = gt[gBeta + i1], ik0 = gt[gIk + i0], ik1 = gt[gIk + i1];
+                sq0 = gt[gSq + i0], sq1 = gt[gSq + i1];
+            }
             uint32_t ao[4], yh[4], yl[4], uh[4], ul[4];
             ldsm4_t(ao, at_n<16>(sr + Rec::o, 0, 2 * rg, lane));
             ldsm4_t(yh, at_n<16>(sr + Rec::y, 0, 2 * rg, lane));
@@ -218,41 +247,58 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
                 uint32_t bh[4], bl[4];
                 ldsm4_t(bh, at_k<16>(sr + Rec::u, 0, 2 * cg, lane));
                 ldsm4_t(bl, at_k<16>(sr + Rec::u + 2048, 0, 2 * cg, lane));
+                if (in_units(E, pe, io * iu)) {
 #pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    float x[4], y[4];
-                    mma0(x, ao, bh[2 * i], bh[2 * i + 1]);
-                    mma0(y, yh, bh[2 * i], bh[2 * i + 1]);
-                    mma(x, ao, bl[2 * i], bl[2 * i + 1]);
-                    mma(y, yl, bh[2 * i], bh[2 * i + 1]);
-                    mma(y, yh, bl[2 * i], bl[2 * i + 1]);
-                    add_scaled(E[i], x, io * iu);
-                    add_scaled(W[i], y, iy * iu);
+                    for (int i = 0; i < 2; i++) mma(E[i], ao, bh[2 * i], bh[2 * i + 1]);
+#pragma unroll
+                    for (int i = 0; i < 2; i++) mma(E[i], ao, bl[2 * i], bl[2 * i + 1]);
+                }
+                if (in_units(W, pw, iy * iu)) {
+#pragma unroll
+                    for (int i = 0; i < 2; i++) mma(W[i], yh, bh[2 * i], bh[2 * i + 1]);
+#pragma unroll
+                    for (int i = 0; i < 2; i++) mma(W[i], yl, bh[2 * i], bh[2 * i + 1]);
+#pragma unroll
+                    for (int i = 0; i < 2; i++) mma(W[i], yh, bl[2 * i], bl[2 * i + 1]);
                 }
             }
             const float is = f[fS + cg / 2], id = f[fDs + cg / 2];
+            const bool tq = in_units(Zq, pq, io * is), tz = in_units(Z, pz, iy * is), tu = in_units(Zw, pu, iu * id);
 #pragma unroll
             for (int p = 0; p < DW / 16; p++) {
-                uint32_t bh[4], bl[4], dh[4], dl[4];
+                uint32_t bh[4], bl[4];
                 const uint32_t off = at_k<16>(0, 0, cg * (DW / 8) + 2 * p, lane);
                 ldsm4_t(bh, sr + Rec::s + off);
                 ldsm4_t(bl, sr + Rec::s + 32 * DK + off);
-                ldsm4_t(dh, sr + Rec::ds + off);
-                ldsm4_t(dl, sr + Rec::ds + 32 * DK + off);
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    float x[4], y[4], z[4];
-                    mma0(x, ao, bh[2 * i], bh[2 * i + 1]);
-                    mma0(y, yh, bh[2 * i], bh[2 * i + 1]);
-                    mma0(z, uh, dh[2 * i], dh[2 * i + 1]);
-                    mma(x, ao, bl[2 * i], bl[2 * i + 1]);
-                    mma(y, yl, bh[2 * i], bh[2 * i + 1]);
-                    mma(z, ul, dh[2 * i], dh[2 * i + 1]);
-                    mma(y, yh, bl[2 * i], bl[2 * i + 1]);
-                    mma(z, uh, dl[2 * i], dl[2 * i + 1]);
-                    add_scaled(Zq[2 * p + i], x, io * is);
-                    add_scaled(Z[2 * p + i], y, iy * is);
-                    add_scaled(Zw[2 * p + i], z, iu * id);
+                float(&q0)[4] = Zq[2 * p], (&q1)[4] = Zq[2 * p + 1], (&z0)[4] = Z[2 * p], (&z1)[4] = Z[2 * p + 1];
+                if (tq) {
+                    mma(q0, ao, bh[0], bh[1]);
+                    mma(q1, ao, bh[2], bh[3]);
+                }
+                if (tz) {
+                    mma(z0, yh, bh[0], bh[1]);
+                    mma(z1, yh, bh[2], bh[3]);
+                }
+                if (tq) {
+                    mma(q0, ao, bl[0], bl[1]);
+                    mma(q1, ao, bl[2], bl[3]);
+                }
+                if (tz) {
+                    mma(z0, yl, bh[0], bh[1]);
+                    mma(z1, yl, bh[2], bh[3]);
+                    mma(z0, yh, bl[0], bl[1]);
+                    mma(z1, yh, bl[2], bl[3]);
+                }
+                ldsm4_t(bh, sr + Rec::ds + off);
+                ldsm4_t(bl, sr + Rec::ds + 32 * DK + off);
+                if (tu) {
+                    float(&u0)[4] = Zw[2 * p], (&u1)[4] = Zw[2 * p + 1];
+                    mma(u0, uh, bh[0], bh[1]);
+                    mma(u1, uh, bh[2], bh[3]);
+                    mma(u0, ul, bh[0], bh[1]);
+                    mma(u1, ul, bh[2], bh[3]);
+                    mma(u0, uh, bl[0], bl[1]);
+                    mma(u1, uh, bl[2], bl[3]);
                 }
             }
             // <dS1, S0> of the share's columns, four of the 16 rows each
@@ -270,27 +316,33 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
                 }
                 inner = fmaf(x, is * id, inner);
             }
-            if (mine) {
+            // dv and Y . v: a share takes every fourth group
+            if ((gr & 3) == cg) {
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     const int row = 16 * rg + g + 8 * (e & 1), col = 16 * gr + 2 * t + 8 * (e >> 1);
+                    const uint32_t v2 = *reinterpret_cast<const uint32_t*>(rec + Gr::oV + row * 32 + 4 * t + 16 * (e >> 1));
                     float2 y = sum_h2(yh[e], yl[e]);
                     y.x *= iy;
                     y.y *= iy;
-                    const float s = (e & 1 ? b1 * k1 : b0 * k0);  // dv = beta' Y / s_k
+                    const float s = (e & 1 ? b1 * ik1 : b0 * ik0);  // dv = beta' Y / s_k
                     if (row < rows && col < a.dv_dim)
                         st_pair(dv + ((row0 + row) * a.H + h) * a.dv_dim + col, s * y.x, s * y.y);
-                    const float d = fmaf(y.x, tc::bf16lo(v2[e]), y.y * tc::bf16hi(v2[e]));
-                    if (e & 1) db1 = fmaf(d, k1, db1);
-                    else db0 = fmaf(d, k0, db0);
+                    const float d = row < L ? fmaf(y.x, tc::bf16lo(v2), y.y * tc::bf16hi(v2)) : 0.f;
+                    if (e & 1) db1 = fmaf(d, ik1, db1);
+                    else db0 = fmaf(d, ik0, db0);
                 }
             }
+            // the last stage of a head holds the gates until its end
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(empty + st);
+            if (lane == 0 && gr < ng - 1) tc::mbar_arrive(empty + st);
         }
+        const double* G = reinterpret_cast<const double*>(reinterpret_cast<const uint8_t*>(gt) + kGates);
 
         // the scores, with the decays, in two terms
         if (cg <= rg) {
+            times(E, pe, pe);
+            times(W, pw, pw);
             float bw[2][4];
 #pragma unroll
             for (int n = 0; n < 2; n++)
@@ -320,28 +372,22 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
             put(W, 1, &inv_w[rg][cg]);
             put(bw, 2, &inv_b[rg][cg]);
         }
-        if (r == 0) wait(&keys, 0);
+        if (r == 0) wait(&keys, done);
         tc::barrier(1, Gr::threads);
 
         const float eg0 = gt[gEG + i0], eg1 = gt[gEG + i1], ec0 = gt[gEC + i0], ec1 = gt[gEC + i1];
         auto pair_at = [&](int off, int row, int n) {
             return unpack_h2(*reinterpret_cast<const uint32_t*>(sm + off + tile_at(row, cg * (DW / 8) + n) + 4 * t));
         };
+        times(Zq, eg0 * pq, eg1 * pq);
+        times(Z, eg0 * pz, eg1 * pz);
+        times(Zw, ec0 * pu, ec1 * pu);
         float ca0 = 0.f, ca1 = 0.f, cc0 = 0.f, cc1 = 0.f;  // row sums of dg
 #pragma unroll
         for (int n = 0; n < DW / 8; n++) {
             const float2 x0 = pair_at(Gr::oK, i0, n), x1 = pair_at(Gr::oK, i1, n);
-            Zq[n][0] *= eg0; Zq[n][1] *= eg0; Zq[n][2] *= eg1; Zq[n][3] *= eg1;
-            Z[n][0] *= eg0; Z[n][1] *= eg0; Z[n][2] *= eg1; Z[n][3] *= eg1;
-            Zw[n][0] *= ec0; Zw[n][1] *= ec0; Zw[n][2] *= ec1; Zw[n][3] *= ec1;
             cc0 = fmaf(x0.x, Zw[n][0], fmaf(x0.y, Zw[n][1], cc0));
             cc1 = fmaf(x1.x, Zw[n][2], fmaf(x1.y, Zw[n][3], cc1));
-            // z into the sum over the value heads; Zw goes on with w
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                dka[n][e] += Zw[n][e];
-                Zw[n][e] = 0.f;
-            }
         }
 #pragma unroll
         for (int ks = 0; ks < 4; ks++) {
@@ -393,7 +439,7 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
                 }
             }
         }
-        // now Zq = dq, -Z = r, Zw = w
+        // now Zq = dq, -Z = r, Zw = z + w
 #pragma unroll
         for (int n = 0; n < DW / 8; n++) {
             const float2 x0 = pair_at(Gr::oK, i0, n), x1 = pair_at(Gr::oK, i1, n);
@@ -403,11 +449,9 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
             db1 += kr1;
             ca0 += q0.x * Zq[n][0] + q0.y * Zq[n][1] + b0 * kr0 - (x0.x * Zw[n][0] + x0.y * Zw[n][1]);
             ca1 += q1.x * Zq[n][2] + q1.y * Zq[n][3] + b1 * kr1 - (x1.x * Zw[n][2] + x1.y * Zw[n][3]);
+            // dk
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                dqa[n][e] += Zq[n][e];
-                dka[n][e] += Zw[n][e] - (e < 2 ? b0 : b1) * Z[n][e];
-            }
+            for (int e = 0; e < 4; e++) Zw[n][e] -= (e < 2 ? b0 : b1) * Z[n][e];
         }
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
@@ -444,7 +488,7 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
                 y[i] = 0.f;
 #pragma unroll
                 for (int j = 0; j < NH; j++) {
-                    x[i] += row_a[j][row];
+                    x[i] += (double)row_a[j][row] + row_c[j][row];  // a took z with w
                     z[i] += row_c[j][row];
                     y[i] += row_b[j][row];
                 }
@@ -472,22 +516,41 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
             }
         }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(gempty + (r & 1));
-    }
-
-    // undo the scaling: any value head's gates hold the keys' and queries' scales
-    const float* gt = reinterpret_cast<const float*>(sm + Gr::oG + ((rep - 1) & 1) * 2048);
+        if (lane == 0) tc::mbar_arrive(empty + (it - 1) % NS);
+        // the sum over the value heads, in their order, through memory that this
+        // thread alone touches (kept in registers over a head they would spill)
+        if (rep > 1) {
+            float4* sum = a.sums + (size_t)item * (C * DK / 2) + tid;
 #pragma unroll
-    for (int half = 0; half < 2; half++) {
-        const int row = half ? i1 : i0;
-        if (row >= rows) continue;
-        const float ik = gt[gIk + row], iq = 1.f / gt[gSq + row];
-#pragma unroll
-        for (int n = 0; n < DW / 8; n++) {
-            const size_t at = ((row0 + row) * a.Hk + hk) * DK + cg * DW + 8 * n + 2 * t;
-            st_pair(dq + at, dqa[n][2 * half] * iq, dqa[n][2 * half + 1] * iq);
-            st_pair(dk + at, dka[n][2 * half] * ik, dka[n][2 * half + 1] * ik);
+            for (int n = 0; n < DW / 8; n++) {
+                float(&x)[4] = Zq[n], (&y)[4] = Zw[n];
+                if (r > 0) {
+                    const float4 u = sum[2 * n * Gr::threads], v = sum[(2 * n + 1) * Gr::threads];
+                    x[0] += u.x, x[1] += u.y, x[2] += u.z, x[3] += u.w;
+                    y[0] += v.x, y[1] += v.y, y[2] += v.z, y[3] += v.w;
+                }
+                if (r < rep - 1) {
+                    sum[2 * n * Gr::threads] = make_float4(x[0], x[1], x[2], x[3]);
+                    sum[(2 * n + 1) * Gr::threads] = make_float4(y[0], y[1], y[2], y[3]);
+                }
+            }
         }
+        if (r < rep - 1) continue;
+        // undo the scaling
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+            const int row = half ? i1 : i0;
+            if (row >= rows) continue;
+            const float ik = half ? ik1 : ik0, iq = 1.f / (half ? sq1 : sq0);
+#pragma unroll
+            for (int n = 0; n < DW / 8; n++) {
+                const size_t at = ((row0 + row) * a.Hk + hk) * DK + cg * DW + 8 * n + 2 * t;
+                st_pair(dq + at, Zq[n][2 * half] * iq, Zq[n][2 * half + 1] * iq);
+                st_pair(dk + at, Zw[n][2 * half] * ik, Zw[n][2 * half + 1] * ik);
+            }
+        }
+    }
+    done++;
     }
 }
 
@@ -495,7 +558,14 @@ template <int DK, typename T>
 ret_status grads(const DeltaArgs& a, const GradArgs& g, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(k_delta_grads<DK, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Grad<DK>::smem);
     if (e != cudaSuccess) return fail(RET_ERR_CUDA, "delta rule gradients: %s", cudaGetErrorString(e));
-    k_delta_grads<DK, T><<<dim3(g.nc, a.Hk, a.B), Grad<DK>::threads, Grad<DK>::smem, s>>>(g);
+    // [B, N, heads, dv] as boxes of 16 columns of a head's chunk; zeros behind N and dv
+    CUtensorMap mv;
+    const uint64_t dims[4] = {(uint64_t)a.dv, (uint64_t)a.H, (uint64_t)a.N, (uint64_t)a.B};
+    const uint64_t strides[3] = {(uint64_t)a.dv * 2, (uint64_t)a.H * a.dv * 2, (uint64_t)a.N * a.H * a.dv * 2};
+    const uint32_t box[4] = {16, 1, (uint32_t)C, 1};
+    if (!make_tmap_bf16(&mv, a.v, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE)) return RET_ERR_CUDA;
+    const long long items = (long long)g.nc * a.Hk * a.B;
+    k_delta_grads<DK, T><<<(unsigned)std::min<long long>(148, items), Grad<DK>::threads, Grad<DK>::smem, s>>>(mv, g);
     return check_launch("delta rule: gradients");
 }
 
@@ -509,26 +579,31 @@ ret_status grads_dk(const DeltaArgs& a, const GradArgs& g, cudaStream_t s) {
 
 using namespace delta;
 
-// The workspace: the tables, then the records of every (sequence, head, chunk).
-size_t delta_backward_ws_bytes(const DeltaArgs& a) {
+// The workspace: the tables, the records of every (sequence, head, chunk), and
+// the sums over the value heads of a key head if it has more than one.
+static size_t records_at(const DeltaArgs& a) { return (table_bytes(a) + 255) / 256 * 256; }
+static size_t sums_at(const DeltaArgs& a) {
     const size_t n = (size_t)a.B * a.H * chunks_of(a.N) * groups_of(a.dv);
-    return (table_bytes(a) + 255) / 256 * 256 + n * record_bytes(a.dk);
+    return (records_at(a) + n * record_bytes(a.dk) + 255) / 256 * 256;
+}
+size_t delta_backward_ws_bytes(const DeltaArgs& a) {
+    return sums_at(a) + (a.H > a.Hk ? (size_t)a.B * a.Hk * chunks_of(a.N) * C * a.dk * 8 : 0);
 }
 
 ret_status launch_delta_backward(const DeltaArgs& a, void* ws, cudaStream_t s) {
     const Tables t = tables_at(a, ws);
-    uint8_t* records = reinterpret_cast<uint8_t*>(ws) + (table_bytes(a) + 255) / 256 * 256;
+    uint8_t* records = reinterpret_cast<uint8_t*>(ws) + records_at(a);
     ret_status st = launch_prep(a, t, s);
     if (st != RET_OK) return st;
     if ((st = launch_chains(a, t, records, s)) != RET_OK) return st;
     GradArgs g{};
     g.tb = t;
     g.lengths = a.lengths;
-    g.v = (const __nv_bfloat16*)a.v;
     g.records = records;
+    g.sums = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(ws) + sums_at(a));
     g.dq = a.dq; g.dk = a.dkk; g.dv = a.dvv;
     g.dg = a.dg; g.dbeta = a.dbeta;
-    g.N = a.N; g.nc = chunks_of(a.N); g.Hk = a.Hk; g.H = a.H; g.dv_dim = a.dv;
+    g.N = a.N; g.nc = chunks_of(a.N); g.Hk = a.Hk; g.H = a.H; g.dv_dim = a.dv; g.B = a.B;
     return a.grad_dt == RET_F32 ? grads_dk<float>(a, g, s) : grads_dk<__nv_bfloat16>(a, g, s);
 }
 
