@@ -19,8 +19,8 @@
 //   * a key k_i = s_i k'_i with |k'_i| in [1, 2) (a query likewise); the rule for
 //     k' has beta' = beta s^2, v' = v / s, u' = s u, and the same S and G;
 //   * S (and its gradient) is scaled by the largest value of a half of its rows,
-//     R and U (dU and Y) by a bound on theirs: the largest of V' and of S, times
-//     that of beta'.  |X| = |S k'| <= 2 sqrt(dk) max |S|, so such a scale leaves
+//     R and U (dU and Y) by a bound on theirs: the largest of beta' V' and of S,
+//     times that of beta'.  |X| = |S k'| <= 2 sqrt(dk) max |S|, so such a scale leaves
 //     R below 2^10, and a value 2^-6 of the bound still has its 22 bits.
 // A bf16 output takes one fp16 term of S, U and P (2^-12, against its own 2^-8).
 #pragma once

@@ -359,11 +359,14 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                 mma_row<0, 4>(X, hi, bk);
                 mma_row<0, 4>(X, lo, bk);
             }
-            // V' of the own quarters and its largest value
+            // beta' V' of the own quarters and its largest value
             float vq[4][4], vm = 0.f;
 #pragma unroll
             for (int n = 0; n < 4; n++) {
-                const float2 ik = *reinterpret_cast<const float2*>(gt + gIk + 16 * (n < 2 ? qa : qb) + 8 * (n & 1) + 2 * t);
+                const int at = 16 * (n < 2 ? qa : qb) + 8 * (n & 1) + 2 * t;
+                float2 ik = *reinterpret_cast<const float2*>(gt + gIk + at);
+                const float2 bt = *reinterpret_cast<const float2*>(gt + gBeta + at);
+                ik.x *= bt.x, ik.y *= bt.y;
                 const uint32_t x = v4[n / 2][2 * (n & 1)], y = v4[n / 2][2 * (n & 1) + 1];
                 vq[n][0] = tc::bf16lo(x) * ik.x, vq[n][1] = tc::bf16hi(x) * ik.y;
                 vq[n][2] = tc::bf16lo(y) * ik.x, vq[n][3] = tc::bf16hi(y) * ik.y;
@@ -383,8 +386,8 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
             take_over(xf, hf, lane, R);
 
             // R^T = beta' (V' - exp(G) X); one scale for R and U of the group
-            const float bound = fmaxf(fmaxf(sh.v_max[2 * cg], sh.v_max[2 * cg + 1]), fmaxf(sh.s_max[2 * cg], sh.s_max[2 * cg + 1])) *
-                                fmaxf(1.f, fmaxf(gt[gMax], gt[gMax + 1]));
+            const float bound = fmaxf(fmaxf(sh.v_max[2 * cg], sh.v_max[2 * cg + 1]),
+                                      fmaxf(sh.s_max[2 * cg], sh.s_max[2 * cg + 1]) * fmaxf(1.f, fmaxf(gt[gMax], gt[gMax + 1])));
             float ui;
             const float us = bound_scale(bound, ui);
 #pragma unroll
@@ -392,10 +395,10 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                 const int at = 16 * (n < 2 ? qa : qb) + 8 * (n & 1) + 2 * t;
                 const float2 eg = *reinterpret_cast<const float2*>(gt + gEG + at);
                 const float2 bt = *reinterpret_cast<const float2*>(gt + gBeta + at);
-                R[n][0] = bt.x * (vq[n][0] - eg.x * R[n][0]);
-                R[n][1] = bt.y * (vq[n][1] - eg.y * R[n][1]);
-                R[n][2] = bt.x * (vq[n][2] - eg.x * R[n][2]);
-                R[n][3] = bt.y * (vq[n][3] - eg.y * R[n][3]);
+                R[n][0] = fmaf(-bt.x * eg.x, R[n][0], vq[n][0]);
+                R[n][1] = fmaf(-bt.y * eg.y, R[n][1], vq[n][1]);
+                R[n][2] = fmaf(-bt.x * eg.x, R[n][2], vq[n][2]);
+                R[n][3] = fmaf(-bt.y * eg.y, R[n][3], vq[n][3]);
             }
 #pragma unroll
             for (int i = 0; i < 2; i++) {

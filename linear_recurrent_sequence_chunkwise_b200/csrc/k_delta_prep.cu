@@ -27,9 +27,9 @@ struct Smem {
 };
 
 // Exponent e with |x| 2^-e in [1, 2) for a row spread over `width` lanes,
-// eight values each (0 for a zero or non-finite row).
+// eight values each (0 for a zero or non-finite row; `none`: a zero row).
 template <int WIDTH>
-__device__ __forceinline__ int row_exponent(const float (&x)[8]) {
+__device__ __forceinline__ int row_exponent(const float (&x)[8], bool& none) {
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(x[i]));
@@ -45,6 +45,7 @@ __device__ __forceinline__ int row_exponent(const float (&x)[8]) {
     }
 #pragma unroll
     for (int o = WIDTH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    none = m == 0.f;
     if (!(m > 0.f) || !(ss < 1e30f)) return 0;
     const int e2 = (((__float_as_int(ss) >> 23) & 255) - 127) >> 1;
     return min(max(em + e2, -60), 60);
@@ -101,7 +102,8 @@ __global__ void __launch_bounds__(kThreads, DK == 256 ? 3 : 4) k_delta_prep(Delt
                 x[2 * e + 1] = tc::bf16hi(v[e]);
             }
         }
-        const int ex = row_exponent<kPieces>(x);
+        bool none;
+        const int ex = row_exponent<kPieces>(x, none);
         const float inv = __int_as_float((127 - ex) << 23);
         uint4 o;
         o.x = pack_h2(x[0] * inv, x[1] * inv);
@@ -111,11 +113,15 @@ __global__ void __launch_bounds__(kThreads, DK == 256 ? 3 : 4) k_delta_prep(Delt
         const uint32_t off = which * 2 * C * DK + tile_at(r, p);
         *reinterpret_cast<uint4*>(sm + off) = o;
         if (keys) *reinterpret_cast<uint4*>(keys + off) = o;
-        if (p == 0) (which ? sq : sk)[r] = __int_as_float((127 + ex) << 23);
+        if (p == 0) (which ? sq : sk)[r] = none && !which ? 0.f : __int_as_float((127 + ex) << 23);
     }
     __syncthreads();
     if (tid < C) {
-        const float s = sk[tid], bh = sb[tid] * s * s;
+        // A zero key takes any scale: one that brings beta v, which such a token
+        // has for its u, near v (beta |k|^2 sets no bound on beta there).
+        float s = sk[tid];
+        if (s == 0.f) s = __int_as_float((127 - min(max((__float_as_int(sb[tid]) >> 23 & 255) - 127, 0), 60)) << 23);
+        const float bh = sb[tid] * s * s;
         float* gt = reinterpret_cast<float*>(tb.gates + ch * kGateRow);
         gt[gEG + tid] = expf((float)sG[tid]);
         gt[gEC + tid] = expf((float)(sG[C - 1] - sG[tid]));
