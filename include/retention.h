@@ -562,9 +562,11 @@ ret_status ret_layernorm_backward(const void* dy, const void* x, const float* me
  *   same buffer.  A sequence split into calls that hand the state on gives
  *   the single call's result up to rounding.
  *   bf16 inputs with dk 64, 128 or 256 and dv a multiple of 8 run in chunks of
- *   64 tokens on the tensor cores; bf16 rounding errors of the state, of the
- *   corrections u and of the scores are carried as a second bf16 term, so the
- *   result is that of fp32 arithmetic on the given inputs.  They need a
+ *   64 tokens on the tensor cores; every computed factor enters a product as
+ *   two fp16 terms (22 bits, scaled by powers of two), so the result is close to
+ *   that of fp32 arithmetic on the given inputs while beta |k|^2 <= 2 (beyond
+ *   that, tables in fp16 may overflow).  A NaN or an infinity in a row that
+ *   counts may reach every row of its chunk.  They need a
  *   workspace (device, 256-byte aligned, overlapping nothing, scratch) of
  *   ret_delta_workspace_bytes(...) bytes.  Other shapes (fp32, other dk or dv)
  *   run token by token on the CUDA cores; the size is 0 for them.

@@ -24,7 +24,9 @@
 // and the five products over dv accumulate in registers; then the 64 x 64
 // scores go through shared memory once, in two terms, to meet K and Q.
 //
-// %FIG%
+// 1 x 4096, 16 heads of 128 / 128: 203 us, 27 us for a chunk and head.  Bound by
+// the latency of 16 warps at 128 registers (IPC 1.5), of which the five products
+// need 8 us; 272 MB of records are read at 1.3 TB/s.
 #include <algorithm>
 
 #include "delta_util.cuh"

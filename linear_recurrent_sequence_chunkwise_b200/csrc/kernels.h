@@ -197,7 +197,8 @@ size_t layernorm_bwd_workspace_bytes(long long rows, int d);
 ret_status launch_layernorm_forward(const LayerNormArgs& a, cudaStream_t s);
 ret_status launch_layernorm_backward(const LayerNormArgs& a, cudaStream_t s);
 
-// The gated delta rule (k_delta_step.cu, k_delta_chunk.cu, k_delta_backward.cu).
+// The gated delta rule (k_delta_step.cu, k_delta_prep.cu, k_delta_chunk.cu,
+// k_delta_backward.cu).
 // Value head h reads key head h / (H / Hk).
 constexpr int kDeltaMaxDk = 256;
 struct DeltaArgs {
