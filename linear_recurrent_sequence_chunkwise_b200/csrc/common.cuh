@@ -47,7 +47,34 @@ cudaError_t read_clear_error_delta(int* flag);
 cudaError_t read_clear_error_delta_grads(int* flag);
 cudaError_t read_clear_error_delta_step(int* flag);
 
+// Launch a kernel that follows another one of the same call on the stream: its
+// blocks may be set up while the last of the other still run, and wait in
+// wait_previous() until all of it is done and visible.
+template <typename... P, typename... A>
+ret_status launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, const char* what, A... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    if (e != cudaSuccess) return fail(RET_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    return check_launch(what);
+}
+
 // ---------------------------------------------------------------- device side
+
+// In the kernel before: the next one's blocks may be set up where there is room
+// (once every block of this one has come here).
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// In the kernel after, before it reads what the one before wrote or writes
+// anything that it reads.
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ float ld_as_float(const float* p, size_t i) { return p[i]; }
 __device__ __forceinline__ float ld_as_float(const __nv_bfloat16* p, size_t i) { return __bfloat162float(p[i]); }

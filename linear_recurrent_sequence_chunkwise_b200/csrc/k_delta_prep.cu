@@ -58,6 +58,7 @@ __device__ __forceinline__ int row_exponent(const float (&x)[8], bool& none) {
 template <int DK>
 __global__ void __launch_bounds__(kThreads, DK == 256 ? 3 : 4) k_delta_prep(DeltaArgs a, Tables tb, int nc) {
     using Sm = Smem<DK>;
+    launch_next();
     extern __shared__ __align__(1024) uint8_t sm[];
     __shared__ double sG[C];
     __shared__ float sb[C], sk[C], sq[C];

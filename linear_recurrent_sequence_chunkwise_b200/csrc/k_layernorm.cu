@@ -17,7 +17,7 @@
 // every block writes one partial row, and a second kernel adds those in a fixed
 // order (the result does not depend on timing).  All sums are fp32.
 //
-// 8192 x 2048 bf16: forward 18.5 us (a warp to a row, 64 elements in a lane: 24
+// 8192 x 2048 bf16: forward 16.5 us (a warp to a row, 64 elements in a lane: 24
 // us; eight warps, 8 elements: 28 us), backward 23 + 4 us for the columns (eight
 // warps, 8 elements: 39 us).
 #include <algorithm>
@@ -116,24 +116,29 @@ __device__ __forceinline__ void ld_w(const W* w, int c, W* f) {
 }
 
 // Sums over the T threads of a group; every thread gets them.  `red`: words of
-// the group, alternating between two halves so that one barrier per sum is
-// enough.  `bar`: the group's named barrier, 0 for a group that is the block
-// (a block with a variable one holds 16 of an SM's 64 barriers: four blocks).
+// the group (zero at the start for `one`), alternating between two halves so that one
+// barrier per sum is enough.  `bar`: the group's named barrier, 0 for a group
+// that is the block (a block with a variable one holds 16 of an SM's 64
+// barriers: four blocks).
+__host__ __device__ constexpr int red_words(int T) { return (T / 32 + 3) / 4 * 4; }
 struct GroupSum {
-    float* red;  // [2][2 T / 32]
+    float* red;  // two halves, 16-byte aligned
     int T, bar, half;
     // For a group of a warp or of the whole block.
     __device__ __forceinline__ float one(float x) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (T == 32) return x;
-        const int nw = T / 32;
-        float* r = next(nw);
+        const int n = red_words(T);
+        float* r = next(n);
         if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = x;
         __syncthreads();
-        x = r[0];
-        for (int i = 1; i < nw; i++) x += r[i];
-        return x;
+        float4 t = *reinterpret_cast<const float4*>(r);
+        for (int i = 4; i < n; i += 4) {
+            const float4 u = *reinterpret_cast<const float4*>(r + i);
+            t.x += u.x, t.y += u.y, t.z += u.z, t.w += u.w;
+        }
+        return (t.x + t.y) + (t.z + t.w);
     }
     // Two sums: half of the lanes goes on with each.
     __device__ __forceinline__ float2 two(float x, float y) {
@@ -146,23 +151,21 @@ struct GroupSum {
             return up ? make_float2(other, s) : make_float2(s, other);
         }
         const int nw = T / 32;
-        float* r = next(nw);
+        float* r = next(2 * nw);
         if ((threadIdx.x & 15) == 0) r[(threadIdx.x % T) >> 4] = s;
-        sync();
+        asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(T) : "memory");
         float2 t = *reinterpret_cast<const float2*>(r);
         for (int i = 1; i < nw; i++) {
             const float2 u = *reinterpret_cast<const float2*>(r + 2 * i);
-            t.x += u.x;
-            t.y += u.y;
+            t.x += u.x, t.y += u.y;
         }
         return t;
     }
-    __device__ __forceinline__ float* next(int nw) {
-        float* r = red + half * 2 * nw;
+    __device__ __forceinline__ float* next(int n) {
+        float* r = red + half * n;
         half ^= 1;
         return r;
     }
-    __device__ __forceinline__ void sync() { asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(T) : "memory"); }
 };
 
 // Two fp32 operations in one instruction.
@@ -193,19 +196,23 @@ __global__ void __launch_bounds__(512) k_ln_forward(const T* __restrict__ x, con
                                                    float* __restrict__ mean_out, float* __restrict__ rstd_out,
                                                    long long rows, int d, float eps, int group) {
     constexpr int P = VEC * NV / 2;
-    __shared__ float red[64];
+    __shared__ __align__(16) float red[2 * red_words(512)];
     const int gi = threadIdx.x / group, lane = threadIdx.x % group, ng = blockDim.x / group;
     GroupSum sum{red, group, 0, 0};
+    if (threadIdx.x < 2 * red_words(512)) red[threadIdx.x] = 0.f;  // before the first sum's barrier by its own writers
+    if (group > 32) __syncthreads();
     const float inv_d = 1.f / d;
     const long long stride = (long long)gridDim.x * ng;
     Raw<T, VEC> raw[NV];
-    auto load = [&](long long r) {
-        const T* xr = x + min(r, rows - 1) * d;
+    const T* xr = x + (long long)(blockIdx.x * ng + gi) * d;  // of the row whose loads come next
+    auto load = [&](bool there) {  // the last row again where there is none: no branch around a load
+        if (!there) xr = x + (rows - 1) * d;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int c = (i * group + lane) * VEC;
             raw[i].load(xr + (FULL ? c : min(c, d - VEC)));
         }
+        xr += stride * d;
     };
     // behind the row's end: zero
     auto inside = [&](float2 f, int p) {
@@ -216,7 +223,7 @@ __global__ void __launch_bounds__(512) k_ln_forward(const T* __restrict__ x, con
         return f;
     };
     long long row = (long long)blockIdx.x * ng + gi;
-    load(row);
+    load(row < rows);
     for (; row < rows; row += stride) {
         float2 f[P], s = both(0.f), v = s;
 #pragma unroll
@@ -224,7 +231,7 @@ __global__ void __launch_bounds__(512) k_ln_forward(const T* __restrict__ x, con
             f[p] = inside(pair_of<T, VEC, NV>(raw, p), p);
             s = add2(s, f[p]);
         }
-        load(row + stride);
+        load(row + stride < rows);
         const float mean = sum.one(s.x + s.y) * inv_d;
         const float2 m2 = both(-mean);
 #pragma unroll
@@ -232,7 +239,7 @@ __global__ void __launch_bounds__(512) k_ln_forward(const T* __restrict__ x, con
             f[p] = inside(add2(f[p], m2), p);
             v = fma2(f[p], f[p], v);
         }
-        const float rstd = 1.f / sqrtf(sum.one(v.x + v.y) * inv_d + eps);
+        const float rstd = rsqrtf(sum.one(v.x + v.y) * inv_d + eps);  // good to 2 units
         if (lane == 0) {
             if (mean_out) mean_out[row] = mean;
             if (rstd_out) rstd_out[row] = rstd;
@@ -268,6 +275,7 @@ __global__ void __launch_bounds__(kBwdMost) k_ln_backward(const T* __restrict__ 
                                                          T* __restrict__ dx, float* __restrict__ part, long long rows,
                                                          int d, int group) {
     constexpr int E = VEC * NV, P = E / 2;
+    launch_next();
     // the next row's loads in flight, where they fit the registers
     constexpr bool kAhead = (FULL && sizeof(T) == 2) || E == 8;
     __shared__ __align__(8) float red[64];
@@ -364,6 +372,7 @@ constexpr int kColWarps = 32;
 __global__ void __launch_bounds__(kColWarps * 32) k_ln_columns(const float* __restrict__ part, int parts, int d,
                                                               float* __restrict__ dgain, float* __restrict__ dbias) {
     __shared__ float s[kColWarps][33];
+    wait_previous();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, n = 2 * d;
     float t = 0.f;
@@ -451,8 +460,8 @@ ret_status bwd(const LayerNormArgs& a, cudaStream_t s) {
                     : a.d == group * kBwdElems && a.gain ? go(k_ln_backward<T, W, V, kBwdElems / V, true>)
                                                          : go(k_ln_backward<T, W, V, kBwdElems / V, false>);
     if (st != RET_OK || !part) return st;
-    k_ln_columns<<<(2 * a.d + 31) / 32, kColWarps * 32, 0, s>>>(part, blocks, a.d, a.dgain, a.dbias);
-    return check_launch("ret_layernorm_backward: columns");
+    return launch_after(k_ln_columns, dim3((2 * a.d + 31) / 32), kColWarps * 32, 0, s, "ret_layernorm_backward: columns", part, blocks, a.d,
+                        a.dgain, a.dbias);
 }
 
 }  // namespace
