@@ -16,12 +16,14 @@
 // gradients of the gates, differences of sums, do not survive).  fp16 has a
 // narrow range, so everything is brought near one by powers of two, which are
 // exact:
-//   * a key k_i = s_i k'_i with |k'_i| in [1, 2) (a query likewise); the rule for
-//     k' has beta' = beta s^2, v' = v / s, u' = s u, and the same S and G;
+//   * a key k_i = s_i k'_i with its largest element in [1, 2) (a query likewise);
+//     the rule for k' has beta' = beta s^2, v' = v / s, u' = s u, and the same S
+//     and G;
 //   * S (and its gradient) is scaled by the largest value of a half of its rows,
 //     R and U (dU and Y) by a bound on theirs: the largest of beta' V' and of S,
-//     times that of beta'.  |X| = |S k'| <= 2 sqrt(dk) max |S|, so such a scale leaves
-//     R below 2^10, and a value 2^-6 of the bound still has its 22 bits.
+//     times that of beta'.  beta' |S k'| <= 2 sqrt(dk) max |S| for beta |k|^2 <= 2,
+//     and |K' dS| <= 2 dk max |dS|: the scale leaves R below 2^10 and dU below
+//     2^14, and a value 2^-6 of the bound still has its 22 bits.
 // A bf16 output takes one fp16 term of S, U and P (2^-12, against its own 2^-8).
 #pragma once
 

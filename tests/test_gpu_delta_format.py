@@ -85,6 +85,30 @@ def test_rows_of_different_magnitude():
     assert err_state(host64(S), Sref) < TOL_SPLIT
 
 
+@pytest.mark.parametrize("dk", [64, 256])
+def test_one_key_with_equal_elements(dk):
+    """The largest products that the scales allow: every key the same, its elements
+    and the state's too, beta |k|^2 = 2, so that the state turns round at each token.
+
+    Tolerance: the factors of a product are off by 2^-22.  A correction sums 64
+    terms T r with |T| = 2: 8 x 2 x 2^-22 = 2^-18 of independent errors; the state
+    sums 64 of those times beta k k = 2: 2^-14 a chunk, less than 2^-13 in three."""
+    B, N, H, dv = 1, 140, 1, 24
+    f, _ = inputs(825, B, N, H, H, dk, dv, "bf16")
+    e = 2 - 2.0 ** -6
+    f["k"] = torch.full_like(f["k"], e)
+    f["beta"] = torch.full_like(f["beta"], 2 / (dk * e ** 2))
+    f["g"] = torch.zeros_like(f["g"])
+    s0, dS = (torch.full((B, H, dk, dv), e) for _ in range(2))
+    ref, Sref = od.delta_forward(**f64(f), initial_state=host64(s0))
+    out, S = forward(cuda(f), s0.cuda())
+    assert err_out(host64(out), ref) < 2.0 ** -13
+    assert err_state(host64(S), Sref) < 2.0 ** -13
+    dout = make_tensor(825, 4, (B, N, H, dv), "bf16")
+    grads = R.ret_delta_backward_chunkwise(**cuda(f), dout=dev(dout), initial_state=s0.cuda(), dfinal_state=dS.cuda())
+    assert all(torch.isfinite(x).all() for x in grads)
+
+
 def test_all_zero_inputs():
     B, N, H, dk, dv = 1, 70, 2, 64, 24
     z = {"q": torch.zeros(B, N, H, dk), "k": torch.zeros(B, N, H, dk), "v": torch.zeros(B, N, H, dv)}
