@@ -565,8 +565,10 @@ ret_status ret_layernorm_backward(const void* dy, const void* x, const float* me
  *   64 tokens on the tensor cores; every computed factor enters a product as
  *   two fp16 terms (22 bits, scaled by powers of two), so the result is close to
  *   that of fp32 arithmetic on the given inputs while beta |k|^2 <= 2 (beyond
- *   that, tables in fp16 may overflow).  A NaN or an infinity in a row that
- *   counts may reach every row of its chunk.  They need a
+ *   that, tables in fp16 may overflow).  The powers of two on the rows of q and
+ *   k end at 2^-60 and 2^60: a row whose largest element is far beyond them
+ *   loses its bits or overflows.  A NaN or an infinity in a row that counts may
+ *   reach every row of its chunk.  They need a
  *   workspace (device, 256-byte aligned, overlapping nothing, scratch) of
  *   ret_delta_workspace_bytes(...) bytes.  Other shapes (fp32, other dk or dv)
  *   run token by token on the CUDA cores; the size is 0 for them.

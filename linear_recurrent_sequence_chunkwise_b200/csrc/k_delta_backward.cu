@@ -9,12 +9,16 @@
 //     z_j  = exp(G_C - G_j) U_j dS1^T
 //     w_j  = sum_{i>=j} E_ij D_ij q_i - sum_{i>j} beta_i W_ij D_ij k_i
 //     dk   = beta r + w + z,  dv = beta Y,  dbeta_i = Y_i . v_i + k_i . r_i.
-// A row's decay multiplies what it reads and divides what it writes, and the
-// last row's also scales the state:
-//     dg_i = sum_{j>=i} (q_j . dq_j + beta_j k_j . r_j - k_j . w_j)
-//            + sum_{j<i} k_j . z_j + exp(G_C) <dS1, S0>
-// (the sums over z cancel up to the rows before i).  Then
-// dq' = dq / s_q and so on undo the scaling.
+// dg_i is the sum of what passes row i: from the state before to rows from i
+// on, from rows before i to the state after, from state to state, from rows to
+// rows (dq0 and r0 are dq and r without their sums over j):
+//     dg_i = sum_{j>=i} (q_j . dq0_j + beta_j k_j . r0_j) + sum_{j<i} k_j . z_j
+//            + exp(G_C) <dS1, S0> + sum_{a>=i>b} X_ab,
+//     X_ab = E_ab D_ab q_a . k_b - beta_a W_ab D_ab k_a . k_b,
+// the last as sums of rows less sums of columns from i on, in 64 bits, where the
+// pairs on one side of i cancel to the bit.  (As row sums of q . dq + beta k . r -
+// k . w, each rounded by itself, they left 2^-22 of |q . dq|: 1% of dg behind a
+// decay of 1e-11.)  Then dq' = dq / s_q and so on undo the scaling.
 //
 // A key head's gradient is the sum over its value heads: one block takes them
 // all, one after the other, so the order is fixed.  Sixteen warps: a row group
@@ -24,9 +28,12 @@
 // and the five products over dv accumulate in registers; then the 64 x 64
 // scores go through shared memory once, in two terms, to meet K and Q.
 //
-// 1 x 4096, 16 heads of 128 / 128: 203 us, 27 us for a chunk and head.  Bound by
+// Each group's products are added in fp32 (in one accumulator over all groups 18
+// us less, but dg off by half as much again: the tensor cores round towards zero).
+//
+// 1 x 4096, 16 heads of 128 / 128: 221 us, 30 us for a chunk and head.  Bound by
 // the latency of 16 warps at 128 registers (IPC 1.5), of which the five products
-// need 8 us; 272 MB of records are read at 1.3 TB/s.
+// need 8 us; 272 MB of records are read at 1.2 TB/s.
 #include <algorithm>
 
 #include "delta_util.cuh"
@@ -68,7 +75,7 @@ struct Grad {
     static constexpr int oR = oE + 6 * kTile;          // the ring
     // a stage: a record, 16 columns of V, the head's gates
     static constexpr int oV = Record<DK>::bytes, oGate = oV + C * 32, stage = (oGate + kGateRow + 127) / 128 * 128;
-    static constexpr int most = 222 * 1024, fit = (most - oR) / stage, stages = fit > 6 ? 6 : fit;
+    static constexpr int most = 218 * 1024, fit = (most - oR) / stage, stages = fit > 6 ? 6 : fit;
     static constexpr int smem = oR + stages * stage + 1024;
 };
 
@@ -82,21 +89,6 @@ __device__ __forceinline__ float2 sum_h2(uint32_t hi, uint32_t lo) {
     return make_float2(h.x + l.x, h.y + l.y);
 }
 
-// Accumulators in units of p, to be added to in units of q: a change of units is
-// exact (powers of two).  False if what is to be added lies more than 2^60 below
-// them, where it changes nothing and the new units would not hold them.
-template <int N>
-__device__ __forceinline__ bool in_units(float (&acc)[N][4], float& p, float q) {
-    if (p == q) return true;
-    const float f = p / q;
-    if (!(f <= 1.1529215e18f)) return false;
-#pragma unroll
-    for (int n = 0; n < N; n++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) acc[n][e] *= f;
-    p = q;
-    return true;
-}
 template <int N>
 __device__ __forceinline__ void times(float (&acc)[N][4], float f0, float f1) {
 #pragma unroll
@@ -114,6 +106,7 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
     __shared__ uint64_t full[NS], empty[NS], keys;
     __shared__ float inv_e[4][4], inv_w[4][4], inv_b[4][4];
     __shared__ float row_a[NH][C], row_c[NH][C], row_b[NH][C], red[Gr::warps];
+    __shared__ double row_x[NH][C], col_x[4][C];  // of X
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int rep = a.H / a.Hk, ng = groups_of(a.dv_dim);
     T* dq = reinterpret_cast<T*>(a.dq);
@@ -223,7 +216,6 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
         float db0 = 0.f, db1 = 0.f;  // Y . v of rows g and g + 8
         float inner = 0.f;           // <dS1, S0>
         float b0 = 0.f, b1 = 0.f;
-        float pe = 0.f, pw = 0.f, pq = 0.f, pz = 0.f, pu = 0.f;  // units of E, W, Zq, Z, Zw
 
         for (int gr = 0; gr < ng; gr++, it++) {
             const int st = it % NS;
@@ -249,58 +241,47 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
                 uint32_t bh[4], bl[4];
                 ldsm4_t(bh, at_k<16>(sr + Rec::u, 0, 2 * cg, lane));
                 ldsm4_t(bl, at_k<16>(sr + Rec::u + 2048, 0, 2 * cg, lane));
-                if (in_units(E, pe, io * iu)) {
+                const float ie = io * iu, iw = iy * iu;
 #pragma unroll
-                    for (int i = 0; i < 2; i++) mma(E[i], ao, bh[2 * i], bh[2 * i + 1]);
-#pragma unroll
-                    for (int i = 0; i < 2; i++) mma(E[i], ao, bl[2 * i], bl[2 * i + 1]);
-                }
-                if (in_units(W, pw, iy * iu)) {
-#pragma unroll
-                    for (int i = 0; i < 2; i++) mma(W[i], yh, bh[2 * i], bh[2 * i + 1]);
-#pragma unroll
-                    for (int i = 0; i < 2; i++) mma(W[i], yl, bh[2 * i], bh[2 * i + 1]);
-#pragma unroll
-                    for (int i = 0; i < 2; i++) mma(W[i], yh, bl[2 * i], bl[2 * i + 1]);
+                for (int i = 0; i < 2; i++) {
+                    float x[4], y[4];
+                    mma0(x, ao, bl[2 * i], bl[2 * i + 1]);
+                    mma0(y, yl, bh[2 * i], bh[2 * i + 1]);
+                    mma(x, ao, bh[2 * i], bh[2 * i + 1]);
+                    mma(y, yh, bl[2 * i], bl[2 * i + 1]);
+                    mma(y, yh, bh[2 * i], bh[2 * i + 1]);
+                    add_scaled(E[i], x, ie);
+                    add_scaled(W[i], y, iw);
                 }
             }
             const float is = f[fS + cg / 2], id = f[fDs + cg / 2];
-            const bool tq = in_units(Zq, pq, io * is), tz = in_units(Z, pz, iy * is), tu = in_units(Zw, pu, iu * id);
+            const float iq = io * is, iz = iy * is, iw = iu * id;
 #pragma unroll
             for (int p = 0; p < DW / 16; p++) {
                 uint32_t bh[4], bl[4];
                 const uint32_t off = at_k<16>(0, 0, cg * (DW / 8) + 2 * p, lane);
                 ldsm4_t(bh, sr + Rec::s + off);
                 ldsm4_t(bl, sr + Rec::s + 32 * DK + off);
-                float(&q0)[4] = Zq[2 * p], (&q1)[4] = Zq[2 * p + 1], (&z0)[4] = Z[2 * p], (&z1)[4] = Z[2 * p + 1];
-                if (tq) {
-                    mma(q0, ao, bh[0], bh[1]);
-                    mma(q1, ao, bh[2], bh[3]);
-                }
-                if (tz) {
-                    mma(z0, yh, bh[0], bh[1]);
-                    mma(z1, yh, bh[2], bh[3]);
-                }
-                if (tq) {
-                    mma(q0, ao, bl[0], bl[1]);
-                    mma(q1, ao, bl[2], bl[3]);
-                }
-                if (tz) {
-                    mma(z0, yl, bh[0], bh[1]);
-                    mma(z1, yl, bh[2], bh[3]);
-                    mma(z0, yh, bl[0], bl[1]);
-                    mma(z1, yh, bl[2], bl[3]);
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    float x[4], y[4];
+                    mma0(x, ao, bl[2 * i], bl[2 * i + 1]);
+                    mma0(y, yl, bh[2 * i], bh[2 * i + 1]);
+                    mma(x, ao, bh[2 * i], bh[2 * i + 1]);
+                    mma(y, yh, bl[2 * i], bl[2 * i + 1]);
+                    mma(y, yh, bh[2 * i], bh[2 * i + 1]);
+                    add_scaled(Zq[2 * p + i], x, iq);
+                    add_scaled(Z[2 * p + i], y, iz);
                 }
                 ldsm4_t(bh, sr + Rec::ds + off);
                 ldsm4_t(bl, sr + Rec::ds + 32 * DK + off);
-                if (tu) {
-                    float(&u0)[4] = Zw[2 * p], (&u1)[4] = Zw[2 * p + 1];
-                    mma(u0, uh, bh[0], bh[1]);
-                    mma(u1, uh, bh[2], bh[3]);
-                    mma(u0, ul, bh[0], bh[1]);
-                    mma(u1, ul, bh[2], bh[3]);
-                    mma(u0, uh, bl[0], bl[1]);
-                    mma(u1, uh, bl[2], bl[3]);
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    float x[4];
+                    mma0(x, ul, bh[2 * i], bh[2 * i + 1]);
+                    mma(x, uh, bl[2 * i], bl[2 * i + 1]);
+                    mma(x, uh, bh[2 * i], bh[2 * i + 1]);
+                    add_scaled(Zw[2 * p + i], x, iw);
                 }
             }
             // <dS1, S0> of the share's columns, four of the 16 rows each
@@ -341,11 +322,27 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
         }
         const double* G = reinterpret_cast<const double*>(reinterpret_cast<const uint8_t*>(gt) + kGates);
 
-        // the scores, with the decays, in two terms
+        if (r == 0) wait(&keys, done);
+        // the scores, with the decays, in two terms; the sums of X
+        double xr[2] = {0.0, 0.0}, xc[4] = {0.0, 0.0, 0.0, 0.0};
         if (cg <= rg) {
-            times(E, pe, pe);
-            times(W, pw, pw);
-            float bw[2][4];
+            float bw[2][4], qk[2][4], kk[2][4];
+#pragma unroll
+            for (int n = 0; n < 2; n++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) qk[n][e] = kk[n][e] = 0.f;
+#pragma unroll 2
+            for (int s = 0; s < DK / 16; s++) {
+                uint32_t aq[4], ak[4], bk[4];
+                ldsm4(aq, at_k(sQ, 16 * rg, 2 * s, lane));
+                ldsm4(ak, at_k(sK, 16 * rg, 2 * s, lane));
+                ldsm4(bk, at_n(sK, 16 * cg, 2 * s, lane));
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    mma(qk[i], aq, bk[2 * i], bk[2 * i + 1]);
+                    mma(kk[i], ak, bk[2 * i], bk[2 * i + 1]);
+                }
+            }
 #pragma unroll
             for (int n = 0; n < 2; n++)
 #pragma unroll
@@ -356,7 +353,18 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
                     E[n][e] = in ? E[n][e] * D : 0.f;
                     W[n][e] = in && i > j ? W[n][e] * D : 0.f;
                     bw[n][e] = W[n][e] * (e < 2 ? b0 : b1);
+                    const double x = fmaf(E[n][e], qk[n][e], -(bw[n][e] * kk[n][e]));
+                    xr[e >> 1] += x;
+                    xc[2 * n + (e & 1)] += x;
                 }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+                for (int i = 0; i < 2; i++) xr[i] += __shfl_xor_sync(0xffffffffu, xr[i], o);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+                for (int i = 0; i < 4; i++) xc[i] += __shfl_xor_sync(0xffffffffu, xc[i], o);
             auto put = [&](float (&x)[2][4], int tile, float* inv) {
                 float v;
                 const float s = scale_of(x[0], x[1], v);
@@ -374,22 +382,29 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
             put(W, 1, &inv_w[rg][cg]);
             put(bw, 2, &inv_b[rg][cg]);
         }
-        if (r == 0) wait(&keys, done);
         tc::barrier(1, Gr::threads);
+        if (t == 0) row_x[cg][i0] = xr[0], row_x[cg][i1] = xr[1];
+        if (g == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) col_x[rg][16 * cg + 8 * (i >> 1) + 2 * t + (i & 1)] = xc[i];
+        }
 
         const float eg0 = gt[gEG + i0], eg1 = gt[gEG + i1], ec0 = gt[gEC + i0], ec1 = gt[gEC + i1];
         auto pair_at = [&](int off, int row, int n) {
             return unpack_h2(*reinterpret_cast<const uint32_t*>(sm + off + tile_at(row, cg * (DW / 8) + n) + 4 * t));
         };
-        times(Zq, eg0 * pq, eg1 * pq);
-        times(Z, eg0 * pz, eg1 * pz);
-        times(Zw, ec0 * pu, ec1 * pu);
+        times(Zq, eg0, eg1);
+        times(Z, eg0, eg1);
+        times(Zw, ec0, ec1);
         float ca0 = 0.f, ca1 = 0.f, cc0 = 0.f, cc1 = 0.f;  // row sums of dg
 #pragma unroll
         for (int n = 0; n < DW / 8; n++) {
             const float2 x0 = pair_at(Gr::oK, i0, n), x1 = pair_at(Gr::oK, i1, n);
             cc0 = fmaf(x0.x, Zw[n][0], fmaf(x0.y, Zw[n][1], cc0));
             cc1 = fmaf(x1.x, Zw[n][2], fmaf(x1.y, Zw[n][3], cc1));
+            const float2 q0 = pair_at(Gr::oQ, i0, n), q1 = pair_at(Gr::oQ, i1, n);
+            ca0 += q0.x * Zq[n][0] + q0.y * Zq[n][1] - b0 * (x0.x * Z[n][0] + x0.y * Z[n][1]);
+            ca1 += q1.x * Zq[n][2] + q1.y * Zq[n][3] - b1 * (x1.x * Z[n][2] + x1.y * Z[n][3]);
         }
 #pragma unroll
         for (int ks = 0; ks < 4; ks++) {
@@ -407,10 +422,10 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
                         float x[4], y[4];
-                        mma0(x, eh, bk[2 * i], bk[2 * i + 1]);
-                        mma0(y, wh, bk[2 * i], bk[2 * i + 1]);
-                        mma(x, el, bk[2 * i], bk[2 * i + 1]);
-                        mma(y, wl, bk[2 * i], bk[2 * i + 1]);
+                        mma0(x, el, bk[2 * i], bk[2 * i + 1]);
+                        mma0(y, wl, bk[2 * i], bk[2 * i + 1]);
+                        mma(x, eh, bk[2 * i], bk[2 * i + 1]);
+                        mma(y, wh, bk[2 * i], bk[2 * i + 1]);
                         add_scaled(Zq[2 * p + i], x, ie);
                         add_scaled(Z[2 * p + i], y, iw);
                     }
@@ -431,10 +446,10 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
                         float x[4], y[4];
-                        mma0(x, eh, bq[2 * i], bq[2 * i + 1]);
-                        mma0(y, wh, bk[2 * i], bk[2 * i + 1]);
-                        mma(x, el, bq[2 * i], bq[2 * i + 1]);
-                        mma(y, wl, bk[2 * i], bk[2 * i + 1]);
+                        mma0(x, el, bq[2 * i], bq[2 * i + 1]);
+                        mma0(y, wl, bk[2 * i], bk[2 * i + 1]);
+                        mma(x, eh, bq[2 * i], bq[2 * i + 1]);
+                        mma(y, wh, bk[2 * i], bk[2 * i + 1]);
                         add_scaled(Zw[2 * p + i], x, ie);
                         add_scaled(Zw[2 * p + i], y, ib);
                     }
@@ -445,12 +460,8 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
 #pragma unroll
         for (int n = 0; n < DW / 8; n++) {
             const float2 x0 = pair_at(Gr::oK, i0, n), x1 = pair_at(Gr::oK, i1, n);
-            const float2 q0 = pair_at(Gr::oQ, i0, n), q1 = pair_at(Gr::oQ, i1, n);
-            const float kr0 = -(x0.x * Z[n][0] + x0.y * Z[n][1]), kr1 = -(x1.x * Z[n][2] + x1.y * Z[n][3]);
-            db0 += kr0;
-            db1 += kr1;
-            ca0 += q0.x * Zq[n][0] + q0.y * Zq[n][1] + b0 * kr0 - (x0.x * Zw[n][0] + x0.y * Zw[n][1]);
-            ca1 += q1.x * Zq[n][2] + q1.y * Zq[n][3] + b1 * kr1 - (x1.x * Zw[n][2] + x1.y * Zw[n][3]);
+            db0 -= x0.x * Z[n][0] + x0.y * Z[n][1];
+            db1 -= x1.x * Z[n][2] + x1.y * Z[n][3];
             // dk
 #pragma unroll
             for (int e = 0; e < 4; e++) Zw[n][e] -= (e < 2 ? b0 : b1) * Z[n][e];
@@ -490,13 +501,13 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
                 y[i] = 0.f;
 #pragma unroll
                 for (int j = 0; j < NH; j++) {
-                    x[i] += (double)row_a[j][row] + row_c[j][row];  // a took z with w
+                    // tiles of X lie on and below the diagonal
+                    x[i] += row_a[j][row] + (16 * j <= row ? row_x[j][row] : 0.0) - (16 * j + 15 >= row ? col_x[j][row] : 0.0);
                     z[i] += row_c[j][row];
                     y[i] += row_b[j][row];
                 }
             }
-            // sum_{j>=i} a_j + sum_{j<i} c_j = (sum of all c) + sum_{j>=i} (a_j - c_j),
-            // kept apart: c's sum over the rows before i is its own scan
+            // sums over the rows from one on, and over those before one
             double s = x[0] + x[1], before = z[0] + z[1];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {

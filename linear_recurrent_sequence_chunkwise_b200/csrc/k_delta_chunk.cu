@@ -218,13 +218,13 @@ __device__ __forceinline__ void state_product(float (&acc)[8][4], const uint32_t
         if (j == 0) {
 #pragma unroll
             for (int i = 0; i < D; i++) {
-                mma0(acc[2 * i], hi[j], b[i][0], b[i][1]);
-                mma0(acc[2 * i + 1], hi[j], b[i][2], b[i][3]);
+                mma0(acc[2 * i], lo[j], b[i][0], b[i][1]);
+                mma0(acc[2 * i + 1], lo[j], b[i][2], b[i][3]);
             }
         } else {
-            mma_row<0, D>(acc, hi[j], b);
+            mma_row<0, D>(acc, lo[j], b);
         }
-        mma_row<0, D>(acc, lo[j], b);
+        mma_row<0, D>(acc, hi[j], b);
     }
 }
 template <int N>
@@ -417,28 +417,33 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
             // U^T = R^T T^T; T is lower triangular: token i takes j <= i
             float U[4][4];
             zero(U);
+            // the small products, then the large ones; for the gradients in passes of
+            // their own (the forward at dk 256: 939 us with, 916 without)
+            constexpr int kPasses = MODE == kKeep ? 2 : 1;
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                if (j > qb) continue;
-                uint32_t rh[4], rl[4], th[2][4], tl[2][4];
-                get4(rf(j), rh, lane);
-                get4(rf(j) + 512, rl, lane);
+            for (int pass = 0; pass < kPasses; pass++)
 #pragma unroll
-                for (int i = 0; i < 2; i++)
-                    if (i || j <= qa) {
-                        ldsm4(th[i], at_n(sT, 16 * (i ? qb : qa), 2 * j, lane));
-                        ldsm4(tl[i], at_n(sT + kTile, 16 * (i ? qb : qa), 2 * j, lane));
-                    }
-#pragma unroll
-                for (int k = 0; k < 3; k++)
+                for (int j = 0; j < 4; j++) {
+                    if (j > qb) continue;
+                    uint32_t rh[4], rl[4], th[2][4], tl[2][4];
+                    get4(rf(j), rh, lane);
+                    if (pass == 0) get4(rf(j) + 512, rl, lane);
 #pragma unroll
                     for (int i = 0; i < 2; i++)
                         if (i || j <= qa) {
-                            const uint32_t(&x)[4] = k == 2 ? tl[i] : th[i];
-                            mma(U[2 * i], k == 1 ? rl : rh, x[0], x[1]);
-                            mma(U[2 * i + 1], k == 1 ? rl : rh, x[2], x[3]);
+                            ldsm4(th[i], at_n(sT, 16 * (i ? qb : qa), 2 * j, lane));
+                            if (pass == 0) ldsm4(tl[i], at_n(sT + kTile, 16 * (i ? qb : qa), 2 * j, lane));
                         }
-            }
+#pragma unroll
+                    for (int k = pass * 2; k < (kPasses == 1 || pass ? 3 : 2); k++)
+#pragma unroll
+                        for (int i = 0; i < 2; i++)
+                            if (i || j <= qa) {
+                                const uint32_t(&x)[4] = k == 1 ? tl[i] : th[i];
+                                mma(U[2 * i], k == 0 ? rl : rh, x[0], x[1]);
+                                mma(U[2 * i + 1], k == 0 ? rl : rh, x[2], x[3]);
+                            }
+                }
             if (c > 0) wait(sh.u_free + cg, c - 1);
 #pragma unroll
             for (int i = 0; i < 2; i++) {
@@ -581,8 +586,6 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                 for (int p = j; p < 4; p++) {
                     uint32_t ph[4];
                     ldsm4(ph, at_n(sP, 16 * p, 2 * j, lane));
-                    mma(O[2 * p], uh, ph[0], ph[1]);
-                    mma(O[2 * p + 1], uh, ph[2], ph[3]);
                     if constexpr (Pl::terms == 2) {
                         uint32_t pl[4];
                         ldsm4(pl, at_n(sP + kTile, 16 * p, 2 * j, lane));
@@ -591,6 +594,8 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                         mma(O[2 * p], uh, pl[0], pl[1]);
                         mma(O[2 * p + 1], uh, pl[2], pl[3]);
                     }
+                    mma(O[2 * p], uh, ph[0], ph[1]);
+                    mma(O[2 * p + 1], uh, ph[2], ph[3]);
                 }
             }
             scale_tokens(O, gt + gSq, ui, t);
@@ -693,8 +698,8 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
                 uint32_t bk[4][4];
 #pragma unroll
                 for (int p = 0; p < 4; p++) ldsm4(bk[p], at_n(sK, 16 * p, 2 * (hf * KH + kk), lane));
-                mma_row<0, 4>(X, hi, bk);
                 mma_row<0, 4>(X, lo, bk);
+                mma_row<0, 4>(X, hi, bk);
             }
             if (lane == 0) {
                 sh.s_inv[2 * cg + hf] = si;
@@ -732,27 +737,29 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
             float Y[4][4];
             zero(Y);
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                if (i < qa) continue;
-                uint32_t uh[4], ul[4], th[2][4], tl[2][4];
-                get4(rf(i), uh, lane);
-                get4(rf(i) + 512, ul, lane);
+            for (int pass = 0; pass < 2; pass++)  // the small products, then the large ones
 #pragma unroll
-                for (int k = 0; k < 2; k++)
-                    if (!k || i >= qb) {
-                        ldsm4_t(th[k], at_k(sT, 16 * i, 2 * (k ? qb : qa), lane));
-                        ldsm4_t(tl[k], at_k(sT + kTile, 16 * i, 2 * (k ? qb : qa), lane));
-                    }
-#pragma unroll
-                for (int m = 0; m < 3; m++)
+                for (int i = 0; i < 4; i++) {
+                    if (i < qa) continue;
+                    uint32_t uh[4], ul[4], th[2][4], tl[2][4];
+                    get4(rf(i), uh, lane);
+                    if (pass == 0) get4(rf(i) + 512, ul, lane);
 #pragma unroll
                     for (int k = 0; k < 2; k++)
                         if (!k || i >= qb) {
-                            const uint32_t(&x)[4] = m == 2 ? tl[k] : th[k];
-                            mma(Y[2 * k], m == 1 ? ul : uh, x[0], x[1]);
-                            mma(Y[2 * k + 1], m == 1 ? ul : uh, x[2], x[3]);
+                            ldsm4_t(th[k], at_k(sT, 16 * i, 2 * (k ? qb : qa), lane));
+                            if (pass == 0) ldsm4_t(tl[k], at_k(sT + kTile, 16 * i, 2 * (k ? qb : qa), lane));
                         }
-            }
+#pragma unroll
+                    for (int m = pass * 2; m < 2 + pass; m++)
+#pragma unroll
+                        for (int k = 0; k < 2; k++)
+                            if (!k || i >= qb) {
+                                const uint32_t(&x)[4] = m == 1 ? tl[k] : th[k];
+                                mma(Y[2 * k], m == 0 ? ul : uh, x[0], x[1]);
+                                mma(Y[2 * k + 1], m == 0 ? ul : uh, x[2], x[3]);
+                            }
+                }
             if (it > 0) wait(sh.u_free + cg, it - 1);
 #pragma unroll
             for (int i = 0; i < 2; i++) {
@@ -905,9 +912,9 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
             float U[8][4];
             zero(U);
 #pragma unroll
-            for (int i = 0; i < 4; i++)
+            for (int k = 1; k >= 0; k--)
 #pragma unroll
-                for (int k = 0; k < 2; k++)
+                for (int i = 0; i < 4; i++)
 #pragma unroll
                     for (int d = 0; d <= i; d++) {
                         uint32_t b[4];

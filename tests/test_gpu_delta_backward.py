@@ -126,6 +126,20 @@ def test_against_differences():
         assert abs(num - exact) < 5 * TOL * np.linalg.norm(host64(grad)) * np.abs(u).max() + 1e-6
 
 
+@pytest.mark.parametrize("N,dk,dv,g", [(1, 64, 40, -25.0), (1, 256, 168, -25.0), (5, 128, 64, -20.0), (66, 64, 64, -20.0)])
+def test_gates_behind_a_strong_decay(N, dk, dv, g):
+    """dg itself, not next to the row products: what passes a decay of e^-25 is
+    e^-25 of them.  It is the sum of four kinds of paths, each off by 2^-17 of its
+    norm; over the heads their norms and the sum's are alike: 4 x 2^-17."""
+    B, H = 2, 4
+    f, s0 = inputs(909, B, N, H, H, dk, dv, "bf16")
+    f["g"] = torch.full_like(f["g"], g)
+    dout, dS = make_tensor(909, 4, (B, N, H, dv), "bf16"), make_tensor(909, 5, (B, H, dk, dv), "f32", 0.3)
+    got = R.ret_delta_backward_chunkwise(**cuda(f), dout=dev(dout), initial_state=s0.cuda(), dfinal_state=dev(dS))
+    ref = od.delta_backward(**f64(f), dout=dout.f64, initial_state=host64(s0), dfinal_state=dS.f64)
+    assert np.linalg.norm(host64(got[3]) - ref["dg"]) < 2.0 ** -15 * np.linalg.norm(ref["dg"])
+
+
 def test_lengths_and_nan_in_padded_rows():
     B, N, Hk, H, dk, dv = 7, 150, 1, 2, 64, 64
     f, s0 = inputs(904, B, N, Hk, H, dk, dv, "bf16")
