@@ -67,6 +67,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
 
 // Barrier of `threads` threads that agrees on a flag: true if all were.
 __device__ __forceinline__ bool barrier_and(int id, int threads, bool ok) {
+    __syncwarp();  // see below
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
@@ -76,8 +77,10 @@ __device__ __forceinline__ bool barrier_and(int id, int threads, bool ok) {
         : "memory");
     return r != 0;
 }
+// Its warps are whole again first: lanes leave a polling loop one by one.
 __device__ __forceinline__ void barrier(int id, int threads) {
-    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+    __syncwarp();
+    asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // --------------------------------------------------------------- fences

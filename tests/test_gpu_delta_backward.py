@@ -140,6 +140,33 @@ def test_gates_behind_a_strong_decay(N, dk, dv, g):
     assert np.linalg.norm(host64(got[3]) - ref["dg"]) < 2.0 ** -15 * np.linalg.norm(ref["dg"])
 
 
+def test_calls_on_several_streams_together():
+    """Calls that share the GPU wait longer within a block; the results stay the
+    same bits.  Blocks of two groups of columns (the first shape) and of one."""
+    sets = []
+    for B, N, Hk, H, dk, dv in ((3, 300, 2, 6, 64, 200), (2, 400, 4, 8, 128, 200), (2, 700, 2, 4, 128, 128), (1, 500, 4, 4, 256, 96)):
+        f, s0 = inputs(910, B, N, Hk, H, dk, dv, "bf16")
+        sets.append((cuda(f), s0.cuda(), dev(make_tensor(910, 4, (B, N, H, dv), "bf16"))))
+
+    def run(c, s0, dout):
+        out, S = R.ret_delta_forward_chunkwise(**c, initial_state=s0, want_final_state=True)
+        return [out, S, *R.ret_delta_backward_chunkwise(**c, dout=dout, initial_state=s0, dfinal_state=s0)]
+
+    ref = [run(*x) for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for _ in range(100):
+        got = []
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got.append([run(*sets[(i + j) % 4]) for j in range(4)])
+        torch.cuda.synchronize()
+        for i in range(4):
+            for j in range(4):
+                for n, (a, b) in enumerate(zip(got[i][j], ref[(i + j) % 4])):
+                    assert torch.equal(a, b), ((i + j) % 4, n)
+
+
 def test_lengths_and_nan_in_padded_rows():
     B, N, Hk, H, dk, dv = 7, 150, 1, 2, 64, 64
     f, s0 = inputs(904, B, N, Hk, H, dk, dv, "bf16")
