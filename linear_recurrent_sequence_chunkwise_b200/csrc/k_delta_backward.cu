@@ -124,12 +124,19 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
         tc::fence_barrier_init();
     }
     __syncthreads();
+    // After a wait that gave up the others are skipped: the barriers stay complete.
     bool ok = true;
-    auto wait = [&](uint64_t* bar, int phase) {  // after one gave up the others are skipped: the barriers stay complete
+    auto wait_lane = [&](uint64_t* bar, int phase) {
         if (ok && !tc::mbar_wait(bar, phase & 1)) {
             ok = false;
             atomicExch(&g_grad_err, kErrTimeout);
         }
+    };
+    // A warp's wait ends in a vote: polling ends lane by lane, and ldmatrix and
+    // mma.sync are defined only for a warp whose lanes execute them together.
+    auto wait = [&](uint64_t* bar, int phase) {
+        wait_lane(bar, phase);
+        ok = __all_sync(0xffffffffu, ok);
     };
     // One lane: the next record, its columns of V and its head's gates into the
     // ring, ahead of the warps.
@@ -145,7 +152,7 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
     auto load = [&]() {
         if (ahead >= items) return;
         uint64_t* bar = full + stage;
-        if (round > 0) wait(empty + stage, round - 1);
+        if (round > 0) wait_lane(empty + stage, round - 1);
         if (ok) {
             uint8_t* st = sm + Gr::oR + stage * Gr::stage;
             tc::mbar_arrive_expect_tx(bar, Rec::bytes + C * 32 + kGateRow);
@@ -220,7 +227,7 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
         for (int gr = 0; gr < ng; gr++, it++) {
             const int st = it % NS;
             if (tid == 0) load();
-            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
             const uint8_t* rec = sm + Gr::oR + st * Gr::stage;
             const uint32_t sr = tc::smem_u32(rec);
             const float* f = reinterpret_cast<const float*>(rec + Rec::f);

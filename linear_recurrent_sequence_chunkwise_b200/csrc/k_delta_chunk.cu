@@ -91,13 +91,24 @@ struct ChainArgs {
 
 // Waits that give up: the error word is set, and the later waits of the warp
 // are skipped, so that it comes to its end (with wrong results) soon.
+// A wait is the whole warp's and ends in a vote.  Polling ends lane by lane, and
+// what comes after it (ldmatrix, mma.sync) is defined only for a warp whose lanes
+// execute it together.
 struct Waits {
-    bool ok = true;
+    bool ok = true;  // the same in all lanes, but for the feeding lane between `lane` and `together`
     __device__ __forceinline__ void operator()(uint64_t* bar, int phase) {
-        if (ok && !tc::mbar_wait(bar, phase & 1)) {
-            ok = false;
-            atomicExch(&g_delta_err, kErrTimeout);
-        }
+        if (!__all_sync(0xffffffffu, !ok || tc::mbar_wait(bar, phase & 1))) give_up();
+    }
+    // One lane's, while the others wait in `together`.
+    __device__ __forceinline__ void lane(uint64_t* bar, int phase) {
+        if (ok && !tc::mbar_wait(bar, phase & 1)) give_up();
+    }
+    __device__ __forceinline__ void together() { ok = __all_sync(0xffffffffu, ok); }
+
+private:
+    __device__ __forceinline__ void give_up() {
+        ok = false;
+        atomicExch(&g_delta_err, kErrTimeout);
     }
 };
 __device__ __forceinline__ void signal(uint64_t* bar, int lane) {
@@ -139,7 +150,7 @@ struct Shared {
 template <typename Pl, int DK>
 __device__ __forceinline__ void load_a(const Shared& r, const ChainArgs& a, size_t key_chunk, size_t chunk, int it,
                                        Waits& wait) {
-    if (it >= Pl::NA) wait(r.ea + it % Pl::NA, it / Pl::NA - 1);
+    if (it >= Pl::NA) wait.lane(r.ea + it % Pl::NA, it / Pl::NA - 1);
     if (!wait.ok) return;
     uint8_t* s = r.sm + (it % Pl::NA) * Pl::A;
     uint64_t* bar = r.fa + it % Pl::NA;
@@ -151,7 +162,7 @@ __device__ __forceinline__ void load_a(const Shared& r, const ChainArgs& a, size
 template <typename Pl, int DK>
 __device__ __forceinline__ void load_b(const Shared& r, const ChainArgs& a, size_t key_chunk, size_t chunk, int it,
                                        Waits& wait) {
-    if (it >= Pl::NB) wait(r.eb + it % Pl::NB, it / Pl::NB - 1);
+    if (it >= Pl::NB) wait.lane(r.eb + it % Pl::NB, it / Pl::NB - 1);
     if (!wait.ok) return;
     uint8_t* s = r.sm + Pl::oB + (it % Pl::NB) * Pl::B;
     uint64_t* bar = r.fb + it % Pl::NB;
@@ -511,7 +522,7 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
             if (MODE != kKeep && nb < n_chunks) load_b<Pl, DK>(sh, a, kc0 + nb, ch0 + nb, nb, wait);
             if (na < n_chunks) load_a<Pl, DK>(sh, a, kc0 + na, ch0 + na, na, wait);
         }
-        __syncwarp();
+        wait.together();
         if (MODE == kKeep && w < 3 * CG) continue;  // only feeds
         if constexpr (MODE == kKeep) {
             // the operand tiles into the chunk's record
@@ -873,7 +884,7 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
             load(n_chunks, it + NB - 1);
             load(it + NA - 1, n_chunks);
         }
-        __syncwarp();
+        wait.together();
         {  // dO' of this chunk: its record's tile, dU0 and Z
             const int c = n_chunks - 1 - it;
             uint8_t* st = sh.sm + Pl::oB + (it % NB) * Pl::B;
