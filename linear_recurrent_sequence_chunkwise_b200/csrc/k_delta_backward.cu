@@ -138,6 +138,13 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
         wait_lane(bar, phase);
         ok = __all_sync(0xffffffffu, ok);
     };
+    // A warp hands a stage back.  It has read it through the generic proxy and the
+    // copies write through the async proxy: the mbarrier alone does not order them.
+    auto release = [&](uint64_t* bar) {
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar);
+    };
     // One lane: the next record, its columns of V and its head's gates into the
     // ring, ahead of the warps.
     int ahead = blockIdx.x, stage = 0, round = 0, group = 0, head = 0, row = 0, seq = 0;
@@ -324,8 +331,7 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
                 }
             }
             // the last stage of a head holds the gates until its end
-            __syncwarp();
-            if (lane == 0 && gr < ng - 1) tc::mbar_arrive(empty + st);
+            if (gr < ng - 1) release(empty + st);
         }
         const double* G = reinterpret_cast<const double*>(reinterpret_cast<const uint8_t*>(gt) + kGates);
 
@@ -493,6 +499,7 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, o);
         if (lane == 0) red[w] = inner;
+        tc::fence_proxy_async_smem();  // behind this barrier the next K and Q come
         tc::barrier(1, Gr::threads);
         if (w == 0) {
             // in 64 bits (the sums cancel): a from a row to the last one, c of the rows before
@@ -535,8 +542,7 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
                 }
             }
         }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(empty + (it - 1) % NS);
+        release(empty + (it - 1) % NS);
         // the sum over the value heads, in their order, through memory that this
         // thread alone touches (kept in registers over a head they would spill)
         if (rep > 1) {

@@ -115,6 +115,13 @@ __device__ __forceinline__ void signal(uint64_t* bar, int lane) {
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(bar);
 }
+// Hands a stage back to the bulk copies.  The warp has read it through the generic
+// proxy and the copy writes through the async proxy: an mbarrier alone does not
+// order the two, and the last ldmatrix could find rows of the stage's next tiles.
+__device__ __forceinline__ void release(uint64_t* bar, int lane) {
+    tc::fence_proxy_async_smem();
+    signal(bar, lane);
+}
 
 // The block's shared memory and barriers: the stages', and for each group a
 // pair (ready, free) for the tiles of S, those of U and the helper's fp32 terms.
@@ -501,7 +508,7 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                         m[e] = fmaxf(m[e], fabsf(S[2 * d + i][e]));
                     }
             }
-            signal(sh.ea + c % NA, lane);
+            release(sh.ea + c % NA, lane);
             m_own = warp_max(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
         }
         if (a.final_state) write_state(S, a.final_state + sb, a.dv, col0 + g, t);
@@ -610,7 +617,7 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                 }
             }
             scale_tokens(O, gt + gSq, ui, t);
-            signal(sh.eb + c % NB, lane);
+            release(sh.eb + c % NB, lane);
             const size_t row0 = (size_t)b * a.N + (size_t)c * C;
             const int L = len - c * C;
             if constexpr (MODE == kOutF32) {
@@ -822,7 +829,7 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
                 }
             }
             signal(sh.z_free + cg, lane);
-            signal(sh.ea + it % NA, lane);
+            release(sh.ea + it % NA, lane);
             m_own = warp_max(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
         }
         if (dinitial) write_state(S, dinitial + sb, a.dv, col0 + g, t);
@@ -951,7 +958,7 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
             }
             if (lane == 0) sh.v_max[2 * cg] = um;
             signal(sh.z_ready + cg, lane);
-            signal(sh.eb + it % NB, lane);
+            release(sh.eb + it % NB, lane);
         }
     }
 }

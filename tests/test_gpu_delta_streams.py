@@ -1,11 +1,13 @@
 """The gated delta rule's calls beside each other on several streams, in every
 form of the chain: blocks of four, two and one groups of columns, bf16 and fp32
-outputs.  Calls that share the GPU wait longer for each other
-within a block (tiles come late, warps poll); the results are the same bits as a
-call's alone."""
+outputs, and the gradients.  Calls that share the GPU wait longer for each other
+within a block (tiles come late, warps poll, a warp's last reads of a stage come
+late); the results are the same bits as a call's alone."""
 import pytest
 import torch
 
+from retention_inputs import make_tensor
+from tests.helpers import dev
 from tests.test_gpu_delta import cuda, inputs
 
 pytestmark = pytest.mark.gpu
@@ -55,3 +57,13 @@ def test_prompts(shapes, out_dtype):
         calls.append(lambda c=c, s0=s0: R.ret_delta_forward_chunkwise(**c, initial_state=s0, out_dtype=out_dtype,
                                                                       want_final_state=True))
     beside_each_other(calls, 60)
+
+
+def test_gradients():
+    calls = []
+    for B, N, Hk, H, dk, dv in ((4, 200, 8, 16, 128, 128), (2, 300, 16, 16, 64, 72), (4, 130, 8, 16, 256, 40), (1, 700, 2, 4, 128, 96)):
+        f, s0 = inputs(932, B, N, Hk, H, dk, dv, "bf16")
+        c, s0, dout = cuda(f), s0.cuda(), dev(make_tensor(932, 4, (B, N, H, dv), "bf16"))
+        calls.append(lambda c=c, s0=s0, dout=dout: R.ret_delta_backward_chunkwise(**c, dout=dout, initial_state=s0,
+                                                                                 dfinal_state=s0))
+    beside_each_other(calls, 40)
