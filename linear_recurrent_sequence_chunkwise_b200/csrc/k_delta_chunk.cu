@@ -60,14 +60,11 @@ struct Plan {
     // Two rings: the chain warps' K', T and gates, and the helpers' Q', P and gates.
     static constexpr int kGateRoom = 1536, keys = 2 * C * DK;
     static constexpr int oT = keys, aGate = oT + 2 * kTile, A = aGate + kGateRoom;
-    static constexpr int pTiles = MODE == kOutBf16 ? kTile : 2 * kTile;
-    static constexpr int oP = keys, bGate = oP + pTiles, B = MODE == kKeep ? 0 : bGate + kGateRoom;
-    // a group's: S in one or two terms, U (Y) the same way, staging of 64 x 16
-    // bf16; between the chain warps parts of X, in whose place each later puts
+    static constexpr int oP = keys, bGate = oP + 2 * kTile, B = MODE == kKeep ? 0 : bGate + kGateRoom;
+    // a group's: S in two terms, U (Y) the same way, staging of 64 x 16 bf16; between the chain warps parts of X, in whose place each later puts
     // its R (dU), and exp(G_C - G) U (exp(G) beta' Y); the backward: Z in fp32,
     // dU0 in fp32
-    static constexpr int terms = MODE == kOutBf16 ? 1 : 2;
-    static constexpr int sHalf = DK / 16 * 512, oU = terms * sHalf, uHalf = 4 * 512, oV = oU + terms * uHalf;
+    static constexpr int sHalf = DK / 16 * 512, oU = 2 * sHalf, uHalf = 4 * 512, oV = oU + 2 * uHalf;
     static constexpr int oX = oV + 2048, oE = oX + 4096;
     static constexpr int oZ = oE + 4096, oD = oZ + (MODE == kBack ? DK * 64 : 0);
     static constexpr int group = oD + (MODE == kBack ? 4096 : 0);
@@ -173,9 +170,9 @@ __device__ __forceinline__ void load_b(const Shared& r, const ChainArgs& a, size
     if (!wait.ok) return;
     uint8_t* s = r.sm + Pl::oB + (it % Pl::NB) * Pl::B;
     uint64_t* bar = r.fb + it % Pl::NB;
-    tc::mbar_arrive_expect_tx(bar, Pl::keys + Pl::pTiles + kGates);
+    tc::mbar_arrive_expect_tx(bar, Pl::keys + 2 * kTile + kGates);
     bulk_load(s, a.tb.keys + key_chunk * (4 * C * DK) + Pl::keys, Pl::keys, bar);
-    bulk_load(s + Pl::oP, a.tb.tiles + chunk * 4 * kTile + 2 * kTile, Pl::pTiles, bar);
+    bulk_load(s + Pl::oP, a.tb.tiles + chunk * 4 * kTile + 2 * kTile, 2 * kTile, bar);
     bulk_load(s + Pl::bGate, a.tb.gates + chunk * kGateRow, kGates, bar);
 }
 
@@ -374,7 +371,7 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                 uint32_t hi[4], lo[4];
                 split_a(S[2 * kk], S[2 * kk + 1], ss, hi, lo);
                 put4(sf + (hf * KH + kk) * 512, hi, lane);
-                if constexpr (Pl::terms == 2) put4(sf + Pl::sHalf + (hf * KH + kk) * 512, lo, lane);
+                put4(sf + Pl::sHalf + (hf * KH + kk) * 512, lo, lane);
                 uint32_t bk[4][4];
 #pragma unroll
                 for (int p = 0; p < 4; p++) ldsm4(bk[p], at_n(sK, 16 * p, 2 * (hf * KH + kk), lane));
@@ -480,7 +477,7 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                 put4(ef + q * 1024 + 512, lo, lane);
                 split_a(U[2 * i], U[2 * i + 1], 1.f, hi, lo);
                 put4(uf + q * 512, hi, lane);
-                if constexpr (Pl::terms == 2) put4(uf + Pl::uHalf + q * 512, lo, lane);
+                put4(uf + Pl::uHalf + q * 512, lo, lane);
             }
             if (lane == 0 && hf == 0) sh.u_inv[cg] = ui;
             signal(sh.u_ready + cg, lane);
@@ -563,8 +560,7 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
             }
             signal(sh.u_free + cg, lane);
         } else {
-            // O^T = s_q (exp(G) S^T Q^T + U^T P^T).  A bf16 output takes one term
-            // of S, U and P (off by 2^-12 at most each, against its own 2^-9).
+            // O^T = s_q (exp(G) S^T Q^T + U^T P^T)
             uint8_t* st = sh.sm + Pl::oB + (c % NB) * Pl::B;
             const uint32_t sQ = tc::smem_u32(st), sP = sQ + Pl::oP;
             const float* gt = reinterpret_cast<const float*>(st + Pl::bGate);
@@ -583,12 +579,12 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                 }
                 uint32_t hi[4], lo[4];
                 get4(sf + kk * 512, hi, lane);
-                if constexpr (Pl::terms == 2) get4(sf + Pl::sHalf + kk * 512, lo, lane);
+                get4(sf + Pl::sHalf + kk * 512, lo, lane);
                 uint32_t bq[4][4];
 #pragma unroll
                 for (int p = 0; p < 4; p++) ldsm4(bq[p], at_n(sQ, 16 * p, 2 * kk, lane));
                 mma_row<0, 4>(O, hi, bq);
-                if constexpr (Pl::terms == 2) mma_row<0, 4>(O, lo, bq);
+                mma_row<0, 4>(O, lo, bq);
             }
             signal(sh.s_free + cg, lane);
             wait(sh.u_ready + cg, c);
@@ -599,12 +595,12 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
             for (int j = 0; j < 4; j++) {
                 uint32_t uh[4], ul[4];
                 get4(uf + j * 512, uh, lane);
-                if constexpr (Pl::terms == 2) get4(uf + Pl::uHalf + j * 512, ul, lane);
+                get4(uf + Pl::uHalf + j * 512, ul, lane);
 #pragma unroll
                 for (int p = j; p < 4; p++) {
                     uint32_t ph[4];
                     ldsm4(ph, at_n(sP, 16 * p, 2 * j, lane));
-                    if constexpr (Pl::terms == 2) {
+                    {
                         uint32_t pl[4];
                         ldsm4(pl, at_n(sP + kTile, 16 * p, 2 * j, lane));
                         mma(O[2 * p], ul, ph[0], ph[1]);
