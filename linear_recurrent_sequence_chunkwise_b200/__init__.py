@@ -688,7 +688,7 @@ def ret_rotary(q, k=None, freqs=None, positions=None, pos_offset: int = 0, layou
     if q_out is k_out is stream is None and freqs is not None and rotary_dim is None and layout in _ROTARY_LAYOUTS:
         r = _binding.rotary(q, k, freqs, positions, pos_offset, layout == "half", scale, inverse)
         if r is not None:
-            return r
+            return r if r.__class__ is not int else _check(r)
     if layout not in _ROTARY_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(_ROTARY_LAYOUTS)} (got {layout!r})")
     if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3])):
@@ -744,7 +744,7 @@ def ret_layernorm_forward(x, gain=None, bias=None, eps: float = 1e-5, out=None, 
     if out is mean is rstd is stream is None:
         r = _binding.layernorm_forward(x, gain, bias, eps, want_stats)
         if r is not None:
-            return r
+            return r if r.__class__ is not int else _check(r)
     if x.dim() < 1 or x.numel() == 0:
         raise ValueError("x must be [..., d] with at least one row")
     d, lead = x.shape[-1], x.shape[:-1]
@@ -777,7 +777,7 @@ def ret_layernorm_backward(dout, x, mean, rstd, gain=None, dx=None, dgain=None, 
     if dx is dgain is dbias is workspace is stream is None and want_weights:
         r = _binding.layernorm_backward(dout, x, mean, rstd, gain)
         if r is not None:
-            return r
+            return r if r.__class__ is not int else _check(r)
     if x.dim() < 1 or x.numel() == 0:
         raise ValueError("x must be [..., d] with at least one row")
     d, lead = x.shape[-1], x.shape[:-1]
@@ -837,7 +837,7 @@ def ret_delta_forward_chunkwise(q, k, v, g, beta, lengths=None, initial_state=No
         r = _binding.delta_forward(q, k, v, g, beta, lengths, initial_state, out,
                                    (out_dtype or q.dtype) is torch.bfloat16, want_final_state)
         if r is not None:
-            return r
+            return r if r.__class__ is not int else _check(r)
     (B, N), Hk, H, dk, dv = _delta_shapes(q, k, v, g, beta, 2)
     _seq_outputs(q, out, final_state, B, N, H, dk, dv, initial_state)
     _buf(lengths, "lengths", (B,), (torch.int32,), q)
@@ -860,7 +860,7 @@ def ret_delta_decode_step(q, k, v, g, beta, state, out=None, out_dtype=None, str
     if out is stream is None and (out_dtype is None or out_dtype in FLOATS):
         r = _binding.delta_decode_step(q, k, v, g, beta, state, out_dtype is torch.bfloat16)
         if r is not None:
-            return r
+            return r if r.__class__ is not int else _check(r)
     (B,), Hk, H, dk, dv = _delta_shapes(q, k, v, g, beta, 1)
     if state is None:
         raise ValueError("state must be float32 [B, H, dk, dv]")
@@ -892,7 +892,7 @@ def ret_delta_backward_chunkwise(q, k, v, g, beta, dout, lengths=None, initial_s
         r = _binding.delta_backward(q, k, v, g, beta, lengths, initial_state, dout, dfinal_state, grad_dtype is torch.bfloat16,
                                     initial_state is not None if want_dinitial_state is None else want_dinitial_state)
         if r is not None:
-            return r
+            return r if r.__class__ is not int else _check(r)
     (B, N), Hk, H, dk_, dv_ = _delta_shapes(q, k, v, g, beta, 2)
     _buf(dout, "dout", (B, N, H, dv_), (q.dtype,), q)
     _buf(initial_state, "initial_state", (B, H, dk_, dv_), F32, q)

@@ -6,8 +6,10 @@
 // no output, workspace or stream is passed in, checks everything that the C ABI
 // cannot see, makes the outputs and calls the C entry point.  It returns None
 // for whatever it does not take (other layouts, devices or types, arguments
-// that do not fit, an error of the entry point): the Python function then goes
-// its general way, which also words the errors.
+// that do not fit): the Python function then goes its general way, which also
+// words the errors.  Once the entry point has been called nothing is done twice (a
+// decode step updates its state): an error status comes back as an int, which the
+// Python function raises.
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
@@ -46,6 +48,7 @@ int device_of(const Tensor& t) {
 }
 
 PyObject* pass() { Py_RETURN_NONE; }
+PyObject* error(ret_status st) { return PyLong_FromLong(st); }
 // A tuple of tensors, None for an undefined one.
 PyObject* tuple(std::initializer_list<Tensor> ts) {
     PyObject* r = PyTuple_New((Py_ssize_t)ts.size());
@@ -81,7 +84,8 @@ struct Delta {
     }
     const int32_t* lens() const { return lengths ? lengths->data_ptr<int32_t>() : nullptr; }
 };
-// Runs f; a C++ exception (no memory, say) becomes None, and the general way meets it again.
+// Runs f; a C++ exception (no memory for an output, say: before the entry point's
+// call) becomes None, and the general way meets it again.
 template <typename F>
 PyObject* guarded(F f) {
     try {
@@ -113,11 +117,12 @@ PyObject* layernorm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
             rstd = make(lead, at::kFloat, dev);
         }
         const Tensor* w = gain ? gain : bias;
-        if (ret_layernorm_forward(x->data_ptr(), gain ? gain->data_ptr() : nullptr, bias ? bias->data_ptr() : nullptr,
+        const ret_status st =
+            ret_layernorm_forward(x->data_ptr(), gain ? gain->data_ptr() : nullptr, bias ? bias->data_ptr() : nullptr,
                                   PyFloat_AS_DOUBLE(a[3]), rows, (int)d, y.data_ptr(),
                                   stats ? mean.data_ptr<float>() : nullptr, stats ? rstd.data_ptr<float>() : nullptr,
-                                  code(*x), w ? code(*w) : RET_F32, stream(dev)) != RET_OK)
-            return pass();
+                                  code(*x), w ? code(*w) : RET_F32, stream(dev));
+        if (st != RET_OK) return error(st);
         return stats ? tuple({y, mean, rstd}) : THPVariable_Wrap(y);
     });
 }
@@ -140,11 +145,12 @@ PyObject* layernorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const size_t need = ret_layernorm_backward_workspace_bytes(rows, (int)d);
         Tensor dx = make(x->sizes(), x->scalar_type(), dev), dgain = make({d}, at::kFloat, dev), dbias = make({d}, at::kFloat, dev);
         Tensor ws = make({(int64_t)need}, at::kByte, dev);
-        if (ret_layernorm_backward(dy->data_ptr(), x->data_ptr(), mean->data_ptr<float>(), rstd->data_ptr<float>(),
+        const ret_status st =
+            ret_layernorm_backward(dy->data_ptr(), x->data_ptr(), mean->data_ptr<float>(), rstd->data_ptr<float>(),
                                    gain ? gain->data_ptr() : nullptr, rows, (int)d, dx.data_ptr(), dgain.data_ptr<float>(),
                                    dbias.data_ptr<float>(), code(*x), gain ? code(*gain) : RET_F32, ws.data_ptr(), need,
-                                   stream(dev)) != RET_OK)
-            return pass();
+                                   stream(dev));
+        if (st != RET_OK) return error(st);
         return tuple({dx, dgain, dbias});
     });
 }
@@ -167,10 +173,11 @@ PyObject* delta_decode_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
             return pass();
         const bool bf16 = PyObject_IsTrue(a[6]) == 1;
         Tensor out = make({B, H, dv}, bf16 ? at::kBFloat16 : at::kFloat, dev);
-        if (ret_delta_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), t[3]->data_ptr<float>(), t[4]->data_ptr<float>(),
+        const ret_status st =
+            ret_delta_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), t[3]->data_ptr<float>(), t[4]->data_ptr<float>(),
                                   state.data_ptr<float>(), out.data_ptr(), stream(dev), (int)B, (int)Hk, (int)H, (int)dk,
-                                  (int)dv, code(q), bf16 ? RET_BF16 : RET_F32) != RET_OK)
-            return pass();
+                                  (int)dv, code(q), bf16 ? RET_BF16 : RET_F32);
+        if (st != RET_OK) return error(st);
         return THPVariable_Wrap(out);
     });
 }
@@ -191,11 +198,12 @@ PyObject* delta_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (PyObject_IsTrue(a[9]) == 1) final_state = make({d.B, d.H, d.dk, d.dv}, at::kFloat, d.dev);
         const size_t need = ret_delta_workspace_bytes(d.B, d.N, d.Hk, d.H, d.dk, d.dv, code(*d.q));
         if (need) ws = make({(int64_t)need}, at::kByte, d.dev);
-        if (ret_delta_forward_chunkwise(d.q->data_ptr(), d.k->data_ptr(), d.v->data_ptr(), fptr(d.g), fptr(d.beta), d.lens(),
+        const ret_status st =
+            ret_delta_forward_chunkwise(d.q->data_ptr(), d.k->data_ptr(), d.v->data_ptr(), fptr(d.g), fptr(d.beta), d.lens(),
                                         fptr(d.state), d.B, d.N, d.Hk, d.H, d.dk, d.dv, out.data_ptr(),
                                         final_state.defined() ? final_state.data_ptr<float>() : nullptr, stream(d.dev),
-                                        code(*d.q), code(out), need ? ws.data_ptr() : nullptr, need) != RET_OK)
-            return pass();
+                                        code(*d.q), code(out), need ? ws.data_ptr() : nullptr, need);
+        if (st != RET_OK) return error(st);
         return final_state.defined() ? tuple({out, final_state}) : THPVariable_Wrap(out);
     });
 }
@@ -216,12 +224,13 @@ PyObject* delta_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Tensor dg = make(d.g->sizes(), at::kFloat, d.dev), dbeta = make(d.g->sizes(), at::kFloat, d.dev), ds0;
         if (PyObject_IsTrue(a[10]) == 1) ds0 = make({d.B, d.H, d.dk, d.dv}, at::kFloat, d.dev);
         Tensor ws = make({(int64_t)need}, at::kByte, d.dev);
-        if (ret_delta_backward_chunkwise(d.q->data_ptr(), d.k->data_ptr(), d.v->data_ptr(), fptr(d.g), fptr(d.beta),
+        const ret_status st =
+            ret_delta_backward_chunkwise(d.q->data_ptr(), d.k->data_ptr(), d.v->data_ptr(), fptr(d.g), fptr(d.beta),
                                          dout->data_ptr(), d.lens(), fptr(d.state), fptr(dfinal), d.B, d.N, d.Hk, d.H, d.dk, d.dv,
                                          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr<float>(),
                                          dbeta.data_ptr<float>(), ds0.defined() ? ds0.data_ptr<float>() : nullptr, stream(d.dev),
-                                         code(*d.q), code(dq), ws.data_ptr(), need) != RET_OK)
-            return pass();
+                                         code(*d.q), code(dq), ws.data_ptr(), need);
+        if (st != RET_OK) return error(st);
         return tuple({dq, dk, dv, dg, dbeta, ds0});
     });
 }
@@ -246,12 +255,13 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (over || std::max(std::max(B, N), std::max(std::max(H, Hk), std::max(d, 2 * freqs->numel()))) > INT32_MAX) return pass();
         Tensor qo = make(q->sizes(), q->scalar_type(), dev), ko;
         if (k) ko = make(k->sizes(), q->scalar_type(), dev);
-        if (ret_rotary(q->data_ptr(), k ? k->data_ptr() : nullptr, qo.data_ptr(), k ? ko.data_ptr() : nullptr, nullptr, nullptr,
+        const ret_status st =
+            ret_rotary(q->data_ptr(), k ? k->data_ptr() : nullptr, qo.data_ptr(), k ? ko.data_ptr() : nullptr, nullptr, nullptr,
                        nullptr, nullptr, freqs->data_ptr<double>(), PyFloat_AS_DOUBLE(a[6]),
                        pos ? pos->data_ptr<int64_t>() : nullptr, offset, PyObject_IsTrue(a[7]) == 1,
                        PyObject_IsTrue(a[5]) == 1 ? RET_ROTARY_HALF : RET_ROTARY_INTERLEAVED, (int)B, (int)N, (int)H, (int)Hk,
-                       (int)d, (int)(2 * freqs->numel()), code(*q), stream(dev)) != RET_OK)
-            return pass();
+                       (int)d, (int)(2 * freqs->numel()), code(*q), stream(dev));
+        if (st != RET_OK) return error(st);
         return k ? tuple({qo, ko}) : THPVariable_Wrap(qo);
     });
 }
