@@ -15,6 +15,8 @@ namespace ret {
 static thread_local char t_err[512] = "";
 
 ret_status fail(ret_status st, const char* fmt, ...) {
+    // The status reports it: left behind, it would be taken for the next launch's.
+    if (st == RET_ERR_CUDA) (void)cudaGetLastError();
     va_list ap;
     va_start(ap, fmt);
     vsnprintf(t_err, sizeof(t_err), fmt, ap);
