@@ -73,7 +73,8 @@ __global__ void __launch_bounds__(kThreads, DK == 256 ? 3 : 4) k_delta_prep(Delt
 #pragma unroll
         for (int i = 0; i < 2; i++) {
             const int r = 2 * lane + i;
-            x[i] = r < L ? (double)fmaxf(a.g[(t0 + r) * a.H + h], kMinG) : 0.0;
+            const float gr = r < L ? a.g[(t0 + r) * a.H + h] : 0.f;
+            x[i] = gr < kMinG ? kMinG : gr;  // a NaN stays one
             sb[r] = r < L ? a.beta[(t0 + r) * a.H + h] : 0.f;
         }
         double s = x[0] + x[1];
