@@ -565,7 +565,10 @@ ret_status ret_layernorm_backward(const void* dy, const void* x, const float* me
  *   64 tokens on the tensor cores; every computed factor enters a product as
  *   two fp16 terms (22 bits, scaled by powers of two), so the result is close to
  *   that of fp32 arithmetic on the given inputs while beta |k|^2 <= 2 (beyond
- *   that, tables in fp16 may overflow).  The powers of two on the rows of q and
+ *   that, tables in fp16 may overflow).  The bits are those of the largest value
+ *   of a chunk's tile: of tokens of one chunk, what decays before the chunk's end
+ *   (its start, in the gradients) to less than 2^-24 of another's part is lost.
+ *   The powers of two on the rows of q and
  *   k end at 2^-60 and 2^60: a row whose largest element is far beyond them
  *   loses its bits or overflows.  A NaN or an infinity in a row that counts may
  *   reach every row of its chunk.  They need a

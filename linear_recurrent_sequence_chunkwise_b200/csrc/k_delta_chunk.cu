@@ -61,9 +61,9 @@ struct Plan {
     static constexpr int kGateRoom = 1536, keys = 2 * C * DK;
     static constexpr int oT = keys, aGate = oT + 2 * kTile, A = aGate + kGateRoom;
     static constexpr int oP = keys, bGate = oP + 2 * kTile, B = MODE == kKeep ? 0 : bGate + kGateRoom;
-    // a group's: S in two terms, U (Y) the same way, staging of 64 x 16 bf16; between the chain warps parts of X, in whose place each later puts
-    // its R (dU), and exp(G_C - G) U (exp(G) beta' Y); the backward: Z in fp32,
-    // dU0 in fp32
+    // a group's: S in two terms, U (Y) the same way, staging of 64 x 16 bf16;
+    // between the chain warps parts of X, in whose place each later puts its R (dU),
+    // and exp(G_C - G) U (exp(G) beta' Y) in fp32; the backward: Z in fp32, dU0 in fp32
     static constexpr int sHalf = DK / 16 * 512, oU = 2 * sHalf, uHalf = 4 * 512, oV = oU + 2 * uHalf;
     static constexpr int oX = oV + 2048, oE = oX + 4096;
     static constexpr int oZ = oE + 4096, oD = oZ + (MODE == kBack ? DK * 64 : 0);
@@ -125,7 +125,7 @@ __device__ __forceinline__ void release(uint64_t* bar, int lane) {
 struct Shared {
     uint8_t* sm;
     uint64_t *fa, *ea, *fb, *eb, *s_ready, *s_free, *u_ready, *u_free, *z_ready, *z_free;
-    float *s_inv, *u_inv, *s_max, *v_max;  // [2] a group, u_inv one
+    float *s_inv, *u_inv, *s_max, *v_max, *e_max;  // [2] a group, u_inv one
     template <typename Pl, int CG>
     __device__ __forceinline__ void init() {
         extern __shared__ uint8_t raw[];
@@ -134,7 +134,7 @@ struct Shared {
         ea = fa + 2, fb = ea + 2, eb = fb + 2, s_ready = eb + 2, s_free = s_ready + 4, u_ready = s_free + 4, u_free = u_ready + 4;
         z_ready = u_free + 4, z_free = z_ready + 4;
         s_inv = reinterpret_cast<float*>(z_free + 4);
-        u_inv = s_inv + 8, s_max = u_inv + 4, v_max = s_max + 8;
+        u_inv = s_inv + 8, s_max = u_inv + 4, v_max = s_max + 8, e_max = v_max + 8;
         if (threadIdx.x == 0) {
             for (int i = 0; i < 2; i++) {
                 tc::mbar_init(fa + i, 1), tc::mbar_init(fb + i, 1);
@@ -256,6 +256,30 @@ __device__ __forceinline__ void scale_tokens(float (&x)[8][4], const float* f, f
         float2 y = *reinterpret_cast<const float2*>(f + 8 * n + 2 * t);
         y.x *= by, y.y *= by;
         x[n][0] *= y.x, x[n][1] *= y.y, x[n][2] *= y.x, x[n][3] *= y.y;
+    }
+}
+// What a chunk adds to the state, tokens times factors in [0, 1]: behind a strong
+// decay far below the tiles that it was computed from, so it is exchanged in fp32
+// and split with a scale of its own.  The own quarters' tiles into the exchange;
+// their largest magnitude.
+__device__ __forceinline__ float put_gated(uint8_t* buf, const float (&x)[4][4], int qa, int qb, int lane) {
+    float m = 0.f;
+#pragma unroll
+    for (int n = 0; n < 4; n++) {
+        *reinterpret_cast<float4*>(buf + (n < 2 ? qa : qb) * 1024 + (n & 1) * 512 + 16 * lane) =
+            make_float4(x[n][0], x[n][1], x[n][2], x[n][3]);
+#pragma unroll
+        for (int e = 0; e < 4; e++) m = fmaxf(m, fabsf(x[n][e]));
+    }
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+}
+__device__ __forceinline__ void get_gated(const uint8_t* buf, float s, int lane, uint32_t (&hi)[4][4], uint32_t (&lo)[4][4]) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const float4 u = *reinterpret_cast<const float4*>(buf + j * 1024 + 16 * lane);
+        const float4 v = *reinterpret_cast<const float4*>(buf + j * 1024 + 512 + 16 * lane);
+        const float x[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
+        split_a(x, y, s, hi[j], lo[j]);
     }
 }
 // The state's tile r = 8 n + 2 t + (e & 1), column g + 8 (e >> 1), from or to [dk, dv].
@@ -460,37 +484,33 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                             }
                 }
             if (c > 0) wait(sh.u_free + cg, c - 1);
+            // U for the helper, exp(G_C - G) U for the state
 #pragma unroll
             for (int i = 0; i < 2; i++) {
                 uint32_t hi[4], lo[4];
                 const int q = i ? qb : qa;
-                // exp(G_C - G) U for the state, U for the helper
-                float E[2][4];
-#pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    const float2 e2 = *reinterpret_cast<const float2*>(gt + gEC + 16 * q + 8 * k + 2 * t);
-                    E[k][0] = U[2 * i + k][0] * e2.x, E[k][1] = U[2 * i + k][1] * e2.y;
-                    E[k][2] = U[2 * i + k][2] * e2.x, E[k][3] = U[2 * i + k][3] * e2.y;
-                }
-                split_a(E[0], E[1], 1.f, hi, lo);
-                put4(ef + q * 1024, hi, lane);
-                put4(ef + q * 1024 + 512, lo, lane);
                 split_a(U[2 * i], U[2 * i + 1], 1.f, hi, lo);
                 put4(uf + q * 512, hi, lane);
                 put4(uf + Pl::uHalf + q * 512, lo, lane);
             }
             if (lane == 0 && hf == 0) sh.u_inv[cg] = ui;
             signal(sh.u_ready + cg, lane);
+#pragma unroll
+            for (int n = 0; n < 4; n++) {
+                const float2 e2 = *reinterpret_cast<const float2*>(gt + gEC + 16 * (n < 2 ? qa : qb) + 8 * (n & 1) + 2 * t);
+                U[n][0] *= e2.x, U[n][1] *= e2.y, U[n][2] *= e2.x, U[n][3] *= e2.y;
+            }
+            const float em = put_gated(ef, U, qa, qb, lane);
+            if (lane == 0) sh.e_max[2 * cg + hf] = em;
             tc::barrier(1 + cg, 64);
 
             // the half's S^T <- exp(G_C) S^T + (exp(G_C - G) U)^T K
             const float eC = gt[gEG + C - 1];
+            float ei;
+            const float es = scale_for(fmaxf(sh.e_max[2 * cg], sh.e_max[2 * cg + 1]), ei);
+            ei *= ui;
             uint32_t uh[4][4], ul[4][4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                get4(ef + j * 1024, uh[j], lane);
-                get4(ef + j * 1024 + 512, ul[j], lane);
-            }
+            get_gated(ef, es, lane, uh, ul);
             float m[4] = {0.f, 0.f, 0.f, 0.f};
             constexpr int D = KH < 4 ? KH : 4;
 #pragma unroll
@@ -501,7 +521,7 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
                 for (int i = 0; i < 2 * D; i++)
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
-                        S[2 * d + i][e] = fmaf(ui, acc[i][e], eC * S[2 * d + i][e]);
+                        S[2 * d + i][e] = fmaf(ei, acc[i][e], eC * S[2 * d + i][e]);
                         m[e] = fmaxf(m[e], fabsf(S[2 * d + i][e]));
                     }
             }
@@ -779,34 +799,30 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
             for (int i = 0; i < 2; i++) {
                 uint32_t hi[4], lo[4];
                 const int q = i ? qb : qa;
-                float E[2][4];
-#pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    const int at = 16 * q + 8 * k + 2 * t;
-                    const float2 eg = *reinterpret_cast<const float2*>(gt + gEG + at);
-                    const float2 bt = *reinterpret_cast<const float2*>(gt + gBeta + at);
-                    E[k][0] = -Y[2 * i + k][0] * (eg.x * bt.x), E[k][1] = -Y[2 * i + k][1] * (eg.y * bt.y);
-                    E[k][2] = -Y[2 * i + k][2] * (eg.x * bt.x), E[k][3] = -Y[2 * i + k][3] * (eg.y * bt.y);
-                }
-                split_a(E[0], E[1], 1.f, hi, lo);
-                put4(ef + q * 1024, hi, lane);
-                put4(ef + q * 1024 + 512, lo, lane);
                 split_a(Y[2 * i], Y[2 * i + 1], 1.f, hi, lo);
                 put4(uf + q * 512, hi, lane);
                 put4(uf + Pl::uHalf + q * 512, lo, lane);
             }
             if (lane == 0 && hf == 0) sh.u_inv[cg] = ui;
             signal(sh.u_ready + cg, lane);
+#pragma unroll
+            for (int n = 0; n < 4; n++) {
+                const int at = 16 * (n < 2 ? qa : qb) + 8 * (n & 1) + 2 * t;
+                const float2 eg = *reinterpret_cast<const float2*>(gt + gEG + at);
+                const float2 bt = *reinterpret_cast<const float2*>(gt + gBeta + at);
+                Y[n][0] *= -eg.x * bt.x, Y[n][1] *= -eg.y * bt.y, Y[n][2] *= -eg.x * bt.x, Y[n][3] *= -eg.y * bt.y;
+            }
+            const float em = put_gated(ef, Y, qa, qb, lane);
+            if (lane == 0) sh.e_max[2 * cg + hf] = em;
             tc::barrier(1 + cg, 64);
 
             // the half's dS^T <- exp(G_C) dS^T + Z - (exp(G) beta' Y)^T K
             const float eC = gt[gEG + C - 1];
+            float ei;
+            const float es = scale_for(fmaxf(sh.e_max[2 * cg], sh.e_max[2 * cg + 1]), ei);
+            ei *= ui;
             uint32_t yh[4][4], yl[4][4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                get4(ef + j * 1024, yh[j], lane);
-                get4(ef + j * 1024 + 512, yl[j], lane);
-            }
+            get_gated(ef, es, lane, yh, yl);
             float m[4] = {0.f, 0.f, 0.f, 0.f};
             constexpr int D = KH < 4 ? KH : 4;
 #pragma unroll
@@ -819,7 +835,7 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
                     const float z[4] = {z4.x, z4.y, z4.z, z4.w};
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
-                        S[2 * d + i][e] = fmaf(ui, acc[i][e], fmaf(eC, S[2 * d + i][e], z[e]));
+                        S[2 * d + i][e] = fmaf(ei, acc[i][e], fmaf(eC, S[2 * d + i][e], z[e]));
                         m[e] = fmaxf(m[e], fabsf(S[2 * d + i][e]));
                     }
                 }
@@ -936,9 +952,11 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
                         mma(U[2 * d], oh[i], b[0], b[1]);
                         mma(U[2 * d + 1], oh[i], b[2], b[3]);
                     }
-            scale_tokens(o, gt + gEG, os, t);
+            scale_tokens(o, gt + gEG, 1.f, t);
+            float zi;  // of the gated rows: behind a strong decay far below dO'
+            const float zs = tiles_scale(o, zi);
 #pragma unroll
-            for (int i = 0; i < 4; i++) split_a(o[2 * i], o[2 * i + 1], 1.f, oh[i], ol[i]);
+            for (int i = 0; i < 4; i++) split_a(o[2 * i], o[2 * i + 1], zs, oh[i], ol[i]);
             const float um = tiles_max(U) * oi;
             if (it > 0) wait(sh.z_free + cg, it - 1);
 #pragma unroll
@@ -950,7 +968,7 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
                 state_product<4>(acc, oh, ol, sQ, d, lane);
 #pragma unroll
                 for (int i = 0; i < 8; i++)
-                    zf[32 * (2 * d + i)] = make_float4(acc[i][0] * oi, acc[i][1] * oi, acc[i][2] * oi, acc[i][3] * oi);
+                    zf[32 * (2 * d + i)] = make_float4(acc[i][0] * zi, acc[i][1] * zi, acc[i][2] * zi, acc[i][3] * zi);
             }
             if (lane == 0) sh.v_max[2 * cg] = um;
             signal(sh.z_ready + cg, lane);
