@@ -15,7 +15,9 @@
 // The backward's column sums: a group keeps its columns' partial sums of dgain
 // and dbias in registers; the groups of a block add theirs in shared memory,
 // every block writes one partial row, and a second kernel adds those in a fixed
-// order (the result does not depend on timing).  All sums are fp32.
+// order (the result does not depend on timing).  Sums are fp32, those of the partial
+// rows 64-bit: a column's longest chain of fp32 additions is a group's rows and a
+// block's groups.
 //
 // 8192 x 2048 bf16: forward 16.5 us (a warp to a row, 64 elements in a lane: 24
 // us; eight warps, 8 elements: 28 us), backward 23 + 4 us for the columns (eight
@@ -367,15 +369,16 @@ __global__ void __launch_bounds__(kBwdMost) k_ln_backward(const T* __restrict__ 
 }
 
 // Adds the partial rows: a block takes 32 columns, warp w the partial rows
-// w, w + 32, ... (all loads of a thread in flight), then the warps' sums in order.
+// w, w + 32, ... (all loads of a thread in flight), then the warps' sums in order; in
+// 64 bits, which costs nothing beside the loads.
 constexpr int kColWarps = 32;
 __global__ void __launch_bounds__(kColWarps * 32) k_ln_columns(const float* __restrict__ part, int parts, int d,
                                                               float* __restrict__ dgain, float* __restrict__ dbias) {
-    __shared__ float s[kColWarps][33];
+    __shared__ double s[kColWarps][33];
     wait_previous();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, n = 2 * d;
-    float t = 0.f;
+    double t = 0.0;
     if (c < n) {
         constexpr int kLoads = (kBwdBlocks + kColWarps - 1) / kColWarps;
         float x[kLoads];
@@ -390,11 +393,11 @@ __global__ void __launch_bounds__(kColWarps * 32) k_ln_columns(const float* __re
     s[w][lane] = t;
     __syncthreads();
     if (w == 0 && c < n) {
-        t = 0.f;
+        t = 0.0;
 #pragma unroll
         for (int i = 0; i < kColWarps; i++) t += s[i][lane];
         float* out = c < d ? dgain : dbias;
-        if (out) out[c < d ? c : c - d] = t;
+        if (out) out[c < d ? c : c - d] = (float)t;
     }
 }
 
