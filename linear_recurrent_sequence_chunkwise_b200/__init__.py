@@ -5,12 +5,14 @@ The functions below carry the C entry points' names and do argument
 marshalling only (torch tensors -> device pointers, sizes, dtypes, the
 current CUDA stream); every step of the computation runs in the CUDA library
 ``libretention.so`` built from ``csrc/``.  There is no fallback: importing
-this package fails if the library is missing, and every call raises
+this package fails if the library or the binding of the short calls is missing,
+and every call raises
 ``RetentionError`` when the library returns an error status.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional, Sequence
 
@@ -123,7 +125,21 @@ def _load_library():
 
 lib = _load_library()
 
-from . import _binding  # noqa: E402  (the short calls without Python on the way; next to the library, built with it)
+
+def _load_binding(path: str):
+    """The short calls without Python on the way: a module built with the library,
+    against one torch (its version is in the file's name)."""
+    if not os.path.exists(path):
+        raise ImportError(
+            f"{path} is missing (torch {torch.__version__}): build it with "
+            "`python linear_recurrent_sequence_chunkwise_b200/build.py` (g++)")
+    spec = importlib.util.spec_from_file_location(__name__ + "._binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+_binding = _load_binding(os.path.join(_HERE, f"_binding-torch{torch.__version__}.so"))
 
 
 def ret_last_error_string() -> str:

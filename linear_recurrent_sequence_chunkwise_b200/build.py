@@ -1,6 +1,6 @@
 """Build step of the CUDA library: compiles every ``csrc/*.cu`` for sm_100a
-into ``libretention.so`` and ``csrc/binding.cpp`` into ``_binding.so`` next to
-this file (in-tree, so they travel with the source tree).  Run as ``python linear_recurrent_sequence_chunkwise_b200/build.py`` (by path:
+into ``libretention.so`` and ``csrc/binding.cpp`` into ``_binding-torch<version>.so``
+next to this file (in-tree, so they travel with the source tree).  Run as ``python linear_recurrent_sequence_chunkwise_b200/build.py`` (by path:
 importing the package loads the library this script builds)."""
 from __future__ import annotations
 
@@ -12,7 +12,6 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libretention.so")
-BINDING = os.path.join(HERE, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -59,10 +58,18 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 8) -> str:
     return LIB
 
 
+def binding_path() -> str:
+    """The Python binding is built against one torch, whose version its name carries:
+    another torch finds none and builds its own."""
+    import torch
+    return os.path.join(HERE, f"_binding-torch{torch.__version__}.so")
+
+
 def _start_binding(force: bool):
     """Start compiling the Python binding of the short calls (g++, against torch's headers)."""
     src, header = os.path.join(HERE, "csrc", "binding.cpp"), os.path.join(ROOT, "include", "retention.h")
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) > max(map(os.path.getmtime, (src, header))):
+    binding = binding_path()
+    if not force and os.path.exists(binding) and os.path.getmtime(binding) > max(map(os.path.getmtime, (src, header))):
         return None
     import sysconfig
     import torch
@@ -81,11 +88,11 @@ def _finish_binding(job):
         return
     obj, torch_lib, p = job
     _wait(("binding.cpp", p), False)
-    tmp = BINDING + f".tmp{os.getpid()}"
+    tmp = binding_path() + f".tmp{os.getpid()}"
     # the library next to it; torch's own are loaded by the time it is imported
     subprocess.check_call(["g++", "-shared", obj, "-o", tmp, "-L" + HERE, "-l:libretention.so", "-L" + torch_lib, "-ltorch_python",
                            "-ltorch_cuda", "-lc10_cuda", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"])
-    os.replace(tmp, BINDING)
+    os.replace(tmp, binding_path())
 
 
 def _wait(item, verbose):

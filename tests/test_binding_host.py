@@ -1,5 +1,9 @@
 """The short calls' direct binding, host side: an error of the entry point is
-raised, never tried again the general way (a decode step would be applied twice)."""
+raised, never tried again the general way (a decode step would be applied twice);
+and the module's file belongs to the torch that it was built against."""
+import importlib.util
+import os
+
 import pytest
 import torch
 
@@ -30,3 +34,19 @@ def test_what_the_binding_does_not_take_goes_the_general_way(monkeypatch, name):
     monkeypatch.setattr(R._binding, name, lambda *a: None)
     with pytest.raises((ValueError, TypeError)):  # a CPU tensor of two dimensions
         CALLS[name](torch.zeros(2, 2))
+
+
+def test_the_file_is_the_running_torchs(monkeypatch):
+    path = R._binding.__file__
+    assert os.path.basename(path) == f"_binding-torch{torch.__version__}.so"
+    spec = importlib.util.spec_from_file_location("_retention_build", os.path.join(os.path.dirname(path), "build.py"))
+    build = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(build)
+    assert build.binding_path() == path
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert build.binding_path() != path and not os.path.exists(build.binding_path())
+
+
+def test_a_missing_file_says_what_to_do(tmp_path):
+    with pytest.raises(ImportError, match="build.py"):
+        R._load_binding(str(tmp_path / "_binding-torch0.so"))
