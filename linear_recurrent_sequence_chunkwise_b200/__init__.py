@@ -635,20 +635,26 @@ def _call(like: torch.Tensor, stream, fn, *args):
         _check(status)
 
 
+def _new(like: torch.Tensor, shape, dtype, stream):
+    """An output or workspace that a call makes itself, on ``like``'s device.  It
+    belongs to the call's stream: on another stream its memory could still be in use
+    by work before it, and be free again (a workspace: when the call returns) before
+    the call's kernels have run."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _workspace(workspace, need: int, like: torch.Tensor, stream):
     """(pointer, bytes) of the caller's workspace, or of a new one, and the
-    tensor that holds it.  A new one belongs to the stream of the call: it is
-    free again when the call returns, before its kernels have run."""
+    tensor that holds it."""
     if workspace is None:
         if not need:
             return None, 0, None
-        if stream is None:
-            workspace = like.new_empty((need,), dtype=torch.uint8)
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=like.device)
-            with torch.cuda.stream(stream):
-                workspace = like.new_empty((need,), dtype=torch.uint8)
+        workspace = _new(like, (need,), torch.uint8, stream)
     else:
         _same_device(like, workspace=workspace)
     return _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace
@@ -724,13 +730,13 @@ def ret_rotary(q, k=None, freqs=None, positions=None, pos_offset: int = 0, layou
     if rotary_dim is not None and 2 * freqs.numel() != rotary_dim:
         raise ValueError(f"freqs has {freqs.numel()} entries, expected {rotary_dim // 2}")
     if q_out is None:
-        q_out = q.new_empty((B, N, H, d))
+        q_out = _new(q, (B, N, H, d), q.dtype, stream)
     else:
         _buf(q_out, "q_out", (B, N, H, d), (q.dtype,), q)
     if k is not None:
         _same_device(q, k=k)
         if k_out is None:
-            k_out = q.new_empty((B, N, Hk, d))
+            k_out = _new(q, (B, N, Hk, d), q.dtype, stream)
         else:
             _buf(k_out, "k_out", (B, N, Hk, d), (q.dtype,), q)
     _buf(positions, "positions", (B, N), (torch.int64,), q)
@@ -767,14 +773,14 @@ def ret_layernorm_forward(x, gain=None, bias=None, eps: float = 1e-5, out=None, 
     rows = x.numel() // d
     w = _weight_dt(x, d, gain, bias)
     if out is None:
-        out = x.new_empty(x.shape)
+        out = _new(x, x.shape, x.dtype, stream)
     else:
         _buf(out, "out", x.shape, (x.dtype,), x)
     _buf(mean, "mean", lead, F32, x)
     _buf(rstd, "rstd", lead, F32, x)
     if want_stats:
-        mean = x.new_empty(lead, dtype=torch.float32) if mean is None else mean
-        rstd = x.new_empty(lead, dtype=torch.float32) if rstd is None else rstd
+        mean = _new(x, lead, torch.float32, stream) if mean is None else mean
+        rstd = _new(x, lead, torch.float32, stream) if rstd is None else rstd
     _call(x, stream, lib.ret_layernorm_forward, _ptr(x, "x"), _ptr(gain, "gain"), _ptr(bias, "bias"), float(eps), rows,
           d, _ptr(out, "out"), _ptr(mean, "mean"), _ptr(rstd, "rstd"), _dt(x.dtype), w, _STREAM)
     return (out, mean, rstd) if mean is not None or rstd is not None else out
@@ -805,12 +811,12 @@ def ret_layernorm_backward(dout, x, mean, rstd, gain=None, dx=None, dgain=None, 
     _buf(dgain, "dgain", (d,), F32, x)
     _buf(dbias, "dbias", (d,), F32, x)
     if dx is None:
-        dx = x.new_empty(x.shape)
+        dx = _new(x, x.shape, x.dtype, stream)
     else:
         _buf(dx, "dx", x.shape, (x.dtype,), x)
     if want_weights:
-        dgain = x.new_empty((d,), dtype=torch.float32) if dgain is None else dgain
-        dbias = x.new_empty((d,), dtype=torch.float32) if dbias is None else dbias
+        dgain = _new(x, (d,), torch.float32, stream) if dgain is None else dgain
+        dbias = _new(x, (d,), torch.float32, stream) if dbias is None else dbias
     wanted = workspace is None and (dgain is not None or dbias is not None)
     need = lib.ret_layernorm_backward_workspace_bytes(rows, d) if wanted else 0
     wp, nbytes, workspace = _workspace(workspace, need, x, stream)
@@ -858,9 +864,9 @@ def ret_delta_forward_chunkwise(q, k, v, g, beta, lengths=None, initial_state=No
     _seq_outputs(q, out, final_state, B, N, H, dk, dv, initial_state)
     _buf(lengths, "lengths", (B,), (torch.int32,), q)
     if out is None:
-        out = q.new_empty((B, N, H, dv), dtype=out_dtype or q.dtype)
+        out = _new(q, (B, N, H, dv), out_dtype or q.dtype, stream)
     if final_state is None and want_final_state:
-        final_state = q.new_empty((B, H, dk, dv), dtype=torch.float32)
+        final_state = _new(q, (B, H, dk, dv), torch.float32, stream)
     need = lib.ret_delta_workspace_bytes(B, N, Hk, H, dk, dv, _dt(q.dtype)) if workspace is None else 0
     wp, nbytes, workspace = _workspace(workspace, need, q, stream)
     _call(q, stream, lib.ret_delta_forward_chunkwise, _ptr(q, "q"), _ptr(k, "k"), _ptr(v, "v"), _ptr(g, "g"),
@@ -882,7 +888,7 @@ def ret_delta_decode_step(q, k, v, g, beta, state, out=None, out_dtype=None, str
         raise ValueError("state must be float32 [B, H, dk, dv]")
     _buf(state, "state", (B, H, dk, dv), F32, q)
     if out is None:
-        out = q.new_empty((B, H, dv), dtype=out_dtype or torch.float32)
+        out = _new(q, (B, H, dv), out_dtype or torch.float32, stream)
     else:
         _buf(out, "out", (B, H, dv), FLOATS, q)
     _call(q, stream, lib.ret_delta_decode_step, _ptr(q, "q"), _ptr(k, "k"), _ptr(v, "v"), _ptr(g, "g"),
@@ -914,19 +920,19 @@ def ret_delta_backward_chunkwise(q, k, v, g, beta, dout, lengths=None, initial_s
     _buf(initial_state, "initial_state", (B, H, dk_, dv_), F32, q)
     _buf(dfinal_state, "dfinal_state", (B, H, dk_, dv_), F32, q)
     _buf(lengths, "lengths", (B,), (torch.int32,), q)
-    dq = q.new_empty((B, N, Hk, dk_), dtype=grad_dtype) if dq is None else dq
+    dq = _new(q, (B, N, Hk, dk_), grad_dtype, stream) if dq is None else dq
     _buf(dq, "dq", (B, N, Hk, dk_), FLOATS, q)
     _buf(dk, "dk", (B, N, Hk, dk_), (dq.dtype,), q)
     _buf(dv, "dv", (B, N, H, dv_), (dq.dtype,), q)
     _buf(dg, "dg", (B, N, H), F32, q)
     _buf(dbeta, "dbeta", (B, N, H), F32, q)
     _buf(dinitial_state, "dinitial_state", (B, H, dk_, dv_), F32, q)
-    dk = dq.new_empty((B, N, Hk, dk_)) if dk is None else dk
-    dv = dq.new_empty((B, N, H, dv_)) if dv is None else dv
-    dg = q.new_empty((B, N, H), dtype=torch.float32) if dg is None else dg
-    dbeta = q.new_empty((B, N, H), dtype=torch.float32) if dbeta is None else dbeta
+    dk = _new(q, (B, N, Hk, dk_), dq.dtype, stream) if dk is None else dk
+    dv = _new(q, (B, N, H, dv_), dq.dtype, stream) if dv is None else dv
+    dg = _new(q, (B, N, H), torch.float32, stream) if dg is None else dg
+    dbeta = _new(q, (B, N, H), torch.float32, stream) if dbeta is None else dbeta
     if dinitial_state is None and (initial_state is not None if want_dinitial_state is None else want_dinitial_state):
-        dinitial_state = q.new_empty((B, H, dk_, dv_), dtype=torch.float32)
+        dinitial_state = _new(q, (B, H, dk_, dv_), torch.float32, stream)
     need = lib.ret_delta_backward_workspace_bytes(B, N, Hk, H, dk_, dv_, _dt(q.dtype)) if workspace is None else 0
     wp, nbytes, workspace = _workspace(workspace, need, q, stream)
     _call(q, stream, lib.ret_delta_backward_chunkwise, _ptr(q, "q"), _ptr(k, "k"), _ptr(v, "v"), _ptr(g, "g"),
