@@ -568,10 +568,9 @@ ret_status ret_layernorm_backward(const void* dy, const void* x, const float* me
  *   that, tables in fp16 may overflow).  The bits are those of the largest value
  *   of a chunk's tile: of tokens of one chunk, what decays before the chunk's end
  *   (its start, in the gradients) to less than 2^-24 of another's part is lost.
- *   The powers of two on the rows of q and
- *   k end at 2^-60 and 2^60: a row whose largest element is far beyond them
- *   loses its bits or overflows.  A NaN or an infinity in a row that counts may
- *   reach every row of its chunk.  They need a
+ *   The powers of two on the rows of q and k end at 2^-60 and 2^60: a row whose
+ *   largest element is far beyond them loses its bits or overflows.  A NaN or an
+ *   infinity in a row that counts may reach every row of its chunk.  They need a
  *   workspace (device, 256-byte aligned, overlapping nothing, scratch) of
  *   ret_delta_workspace_bytes(...) bytes.  Other shapes (fp32, other dk or dv)
  *   run token by token on the CUDA cores; the size is 0 for them.
@@ -590,7 +589,8 @@ ret_status ret_layernorm_backward(const void* dy, const void* x, const float* me
  *   again and kept in the workspace (device, 256-byte aligned, overlapping
  *   nothing) of ret_delta_backward_workspace_bytes(...) bytes.  bf16 inputs with
  *   dk 64, 128 or 256 and dv a multiple of 8, else RET_ERR_UNSUPPORTED (the size
- *   is 0 then).  All pointers aligned as for the forward, gradients 16-byte.
+ *   is 0 then), H / Hk * dv below 2^25.  All pointers aligned as for the forward,
+ *   gradients 16-byte.
  */
 size_t ret_delta_workspace_bytes(int B, int N, int Hk, int H, int dk, int dv, ret_dtype in_dt);
 

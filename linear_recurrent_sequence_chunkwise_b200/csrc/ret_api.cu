@@ -1053,6 +1053,8 @@ ret_status ret_delta_backward_chunkwise(const void* q, const void* k, const void
         return fail(RET_ERR_INVALID_ARG, "%s: NULL dout, dq, dk, dv, dg or dbeta", who);
     if (!is_dtype(grad_dt)) return fail(RET_ERR_INVALID_ARG, "%s: unknown dtype", who);
     if (B > 32767) return fail(RET_ERR_INVALID_ARG, "%s: at most 32767 sequences", who);
+    if ((long long)(H / Hk) * dv >= (1ll << 25))  // elements of a key head's chunk are counted in 32 bits
+        return fail(RET_ERR_INVALID_ARG, "%s: H / Hk * dv must be below 2^25", who);
     for (const void* p : {dout, (const void*)dfinal_state, (const void*)dq, (const void*)dk_out, (const void*)dv_out,
                           (const void*)dg, (const void*)dbeta, (const void*)dinitial_state})
         if (!aligned(p, 16)) return fail(RET_ERR_INVALID_ARG, "%s: dout and the gradients must be 16-byte aligned", who);
