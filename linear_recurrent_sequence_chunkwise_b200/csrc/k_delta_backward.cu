@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
     extern __shared__ uint8_t raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     __shared__ uint64_t full[NS], empty[NS], keys;
+    __shared__ int filled, asked;  // thread 0's: stages, and K and Q, that it asked for
     __shared__ float inv_e[4][4], inv_w[4][4], inv_b[4][4];
     __shared__ float row_a[NH][C], row_c[NH][C], row_b[NH][C], red[Gr::warps];
     __shared__ double row_x[NH][C], col_x[4][C];  // of X
@@ -121,6 +122,7 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
     if (tid == 0) {
         for (int i = 0; i < NS; i++) tc::mbar_init(full + i, 1), tc::mbar_init(empty + i, Gr::warps);
         tc::mbar_init(&keys, 1);
+        filled = asked = 0;
         tc::fence_barrier_init();
     }
     __syncthreads();
@@ -161,6 +163,7 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
         uint64_t* bar = full + stage;
         if (round > 0) wait_lane(empty + stage, round - 1);
         if (ok) {
+            filled++;
             uint8_t* st = sm + Gr::oR + stage * Gr::stage;
             tc::mbar_arrive_expect_tx(bar, Rec::bytes + C * 32 + kGateRow);
             bulk_load(st, a.records + (chunk * ng + group) * Rec::bytes, Rec::bytes, bar);
@@ -209,6 +212,7 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
         continue;
     }
     if (tid == 0 && ok) {  // K and Q: the last item's readers have passed its last barrier
+        asked++;
         tc::mbar_arrive_expect_tx(&keys, 4 * C * DK);
         bulk_load(sm, a.tb.keys + (((size_t)b * a.Hk + hk) * a.nc + c) * (4 * C * DK), 4 * C * DK, &keys);
     }
@@ -577,6 +581,12 @@ __global__ void __launch_bounds__(Grad<DK>::threads, 1) k_delta_grads(const __gr
         }
     }
     done++;
+    }
+    // No copy of the block's is in flight when it ends: warp 0 has seen all that it
+    // asked for, unless it gave up a wait.
+    if (tid == 0 && !ok) {
+        for (int i = max(filled - NS, 0); i < filled; i++) tc::mbar_wait(full + i % NS, (i / NS) & 1);
+        if (asked) tc::mbar_wait(&keys, (asked - 1) & 1);
     }
 }
 

@@ -150,12 +150,14 @@ struct Shared {
     }
 };
 
-// One lane: the tiles of a chunk, the it-th that is walked, into the rings.
+// One lane: the tiles of a chunk, the it-th that is walked, into the rings; `to`
+// counts the chunks under way.
 template <typename Pl, int DK>
 __device__ __forceinline__ void load_a(const Shared& r, const ChainArgs& a, size_t key_chunk, size_t chunk, int it,
-                                       Waits& wait) {
+                                       Waits& wait, int& to) {
     if (it >= Pl::NA) wait.lane(r.ea + it % Pl::NA, it / Pl::NA - 1);
     if (!wait.ok) return;
+    to = it + 1;
     uint8_t* s = r.sm + (it % Pl::NA) * Pl::A;
     uint64_t* bar = r.fa + it % Pl::NA;
     tc::mbar_arrive_expect_tx(bar, Pl::keys + 2 * kTile + kGates);
@@ -165,15 +167,23 @@ __device__ __forceinline__ void load_a(const Shared& r, const ChainArgs& a, size
 }
 template <typename Pl, int DK>
 __device__ __forceinline__ void load_b(const Shared& r, const ChainArgs& a, size_t key_chunk, size_t chunk, int it,
-                                       Waits& wait) {
+                                       Waits& wait, int& to) {
     if (it >= Pl::NB) wait.lane(r.eb + it % Pl::NB, it / Pl::NB - 1);
     if (!wait.ok) return;
+    to = it + 1;
     uint8_t* s = r.sm + Pl::oB + (it % Pl::NB) * Pl::B;
     uint64_t* bar = r.fb + it % Pl::NB;
     tc::mbar_arrive_expect_tx(bar, Pl::keys + 2 * kTile + kGates);
     bulk_load(s, a.tb.keys + key_chunk * (4 * C * DK) + Pl::keys, Pl::keys, bar);
     bulk_load(s + Pl::oP, a.tb.tiles + chunk * 4 * kTile + 2 * kTile, 2 * kTile, bar);
     bulk_load(s + Pl::bGate, a.tb.gates + chunk * kGateRow, kGates, bar);
+}
+// The feeding lane, last: no copy of the block's is in flight when it ends, not even
+// where a warp gave up a wait and did not see its tiles come.
+template <typename Pl>
+__device__ __forceinline__ void settle(const Shared& r, int to_a, int to_b) {
+    for (int i = max(to_a - Pl::NA, 0); i < to_a; i++) tc::mbar_wait(r.fa + i % Pl::NA, (i / Pl::NA) & 1);
+    for (int i = max(to_b - Pl::NB, 0); i < to_b; i++) tc::mbar_wait(r.fb + i % Pl::NB, (i / Pl::NB) & 1);
 }
 
 __device__ __forceinline__ void put4(uint8_t* p, const uint32_t (&r)[4], int lane) {
@@ -536,15 +546,16 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
     const int hk = h / (a.H / a.Hk);
     const size_t kc0 = ((size_t)b * a.Hk + hk) * a.nc;
     const bool feeds = w == 2 * CG && lane == 0;
+    int to_a = 0, to_b = 0;
     if (feeds)
-        for (int c = 0; c < NA - 1 && c < n_chunks; c++) load_a<Pl, DK>(sh, a, kc0 + c, ch0 + c, c, wait);
+        for (int c = 0; c < NA - 1 && c < n_chunks; c++) load_a<Pl, DK>(sh, a, kc0 + c, ch0 + c, c, wait, to_a);
     if (MODE != kKeep && feeds)
-        for (int c = 0; c < NB - 1 && c < n_chunks; c++) load_b<Pl, DK>(sh, a, kc0 + c, ch0 + c, c, wait);
+        for (int c = 0; c < NB - 1 && c < n_chunks; c++) load_b<Pl, DK>(sh, a, kc0 + c, ch0 + c, c, wait, to_b);
     for (int c = 0; c < n_chunks; c++) {
         if (feeds) {
             const int na = c + NA - 1, nb = c + NB - 1;
-            if (MODE != kKeep && nb < n_chunks) load_b<Pl, DK>(sh, a, kc0 + nb, ch0 + nb, nb, wait);
-            if (na < n_chunks) load_a<Pl, DK>(sh, a, kc0 + na, ch0 + na, na, wait);
+            if (MODE != kKeep && nb < n_chunks) load_b<Pl, DK>(sh, a, kc0 + nb, ch0 + nb, nb, wait, to_b);
+            if (na < n_chunks) load_a<Pl, DK>(sh, a, kc0 + na, ch0 + na, na, wait, to_a);
         }
         wait.together();
         if (MODE == kKeep && w < 3 * CG) continue;  // only feeds
@@ -675,6 +686,7 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
             }
         }
     }
+    if (feeds) settle<Pl>(sh, to_a, to_b);
 }
 
 // ------------------------------------------------------- the backward's chain
@@ -885,9 +897,10 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
     const int hk = h / (a.H / a.Hk);
     const size_t kc0 = ((size_t)b * a.Hk + hk) * a.nc;
     const bool feeds = w == 2 * CG && lane == 0;
+    int to_a = 0, to_b = 0;
     auto load = [&](int na, int nb) {
-        if (na < n_chunks) load_a<Pl, DK>(sh, a, kc0 + n_chunks - 1 - na, ch0 + n_chunks - 1 - na, na, wait);
-        if (nb < n_chunks) load_b<Pl, DK>(sh, a, kc0 + n_chunks - 1 - nb, ch0 + n_chunks - 1 - nb, nb, wait);
+        if (na < n_chunks) load_a<Pl, DK>(sh, a, kc0 + n_chunks - 1 - na, ch0 + n_chunks - 1 - na, na, wait, to_a);
+        if (nb < n_chunks) load_b<Pl, DK>(sh, a, kc0 + n_chunks - 1 - nb, ch0 + n_chunks - 1 - nb, nb, wait, to_b);
     };
     if (feeds) {
         for (int it = 0; it < NB - 1; it++) load(n_chunks, it);
@@ -975,6 +988,7 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
             release(sh.eb + it % NB, lane);
         }
     }
+    if (feeds) settle<Pl>(sh, to_a, to_b);
 }
 
 // ------------------------------------------------------------------ kernels

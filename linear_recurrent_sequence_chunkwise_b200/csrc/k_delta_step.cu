@@ -203,8 +203,11 @@ __global__ void __launch_bounds__(kRingGroups * kRingWarps * 32, 1)
         const float a = expf(gn), bt = bn;
         fetch(i + kRingGroups);
         const bool ok = tc::mbar_wait(full + i % NS, (i / NS) & 1);
-        if (!tc::barrier_and(1 + gi, kThreads, ok)) {  // the group leaves; its stores are waited for below
-            if (tid == 0) atomicExch(&g_step_err, kErrTimeout);
+        if (!tc::barrier_and(1 + gi, kThreads, ok)) {  // the group leaves, behind its loads; its stores are waited for below
+            if (tid == 0) {
+                atomicExch(&g_step_err, kErrTimeout);
+                for (int j = i; j < i + kAhead && j < n; j += kRingGroups) tc::mbar_wait(full + j % NS, (j / NS) & 1);
+            }
             break;
         }
         float4* S = reinterpret_cast<float4*>(sm + (i % NS) * kStage) + row0 * (kRingCols / 4) + (lane & 7);
