@@ -31,9 +31,10 @@
 // Each group's products are added in fp32 (in one accumulator over all groups 18
 // us less, but dg off by half as much again: the tensor cores round towards zero).
 //
-// 1 x 4096, 16 heads of 128 / 128: 221 us, 30 us for a chunk and head.  Bound by
-// the latency of 16 warps at 128 registers (IPC 1.5), of which the five products
-// need 8 us; 272 MB of records are read at 1.2 TB/s.
+// 1 x 4096, 16 heads of 128 / 128: 232 us, 31 us for a chunk and head (221 us before
+// the fences and votes).  Bound by the latency of 16 warps at 128 registers (IPC 1.5;
+// 264 bytes of spills a thread at dk 128, 24 at 64, 1,700 at 256), of which the five
+// products need 8 us; 272 MB of records are read at 1.2 TB/s.
 #include <algorithm>
 
 #include "delta_util.cuh"

@@ -13,7 +13,7 @@
 // triangular, so both have the same work).  They exchange parts of X, R and U
 // through shared memory, with three barriers of 64 threads in a chunk.  (One
 // warp alone takes 8,700 clocks for a chunk of dk = 128, of which the tensor pipe
-// needs 2,600: the halves take 898 to 800 us at 1 x 8192 x 16 x 256 x 512.)
+// needs 2,600; the halves took 898 to 800 us at 1 x 8192 x 16 x 256 x 512.)
 // Everything that the recurrence does not wait for is the third warp's, the
 // helper: the outputs (Q S and P U), or in the backward pass the terms of dO,
 // where a fourth warp writes the records.  They get the operand tiles of S and U
@@ -23,10 +23,16 @@
 // a trip out and back for each of the four products of a chunk.
 // K', Q', T, P come by bulk copies into a ring of stages, issued by a helper.
 //
-// 1 x 8192, 16 heads of 256 / 512: 128 blocks of four groups, 800 us, 6.3 us a
-// chunk (tensor pipe 5,900 of 12,000 clocks).  4 x 2047, 16 heads of 128 / 128:
-// 140 us, 4.4 us a chunk of the longest sequence.  The backward's chains of
-// 1 x 4096, 16 heads of 128 / 128: 285 us.
+// A stage is handed back behind a proxy fence (see release) and every wait of a
+// warp ends in a vote (see Waits).
+//
+// 1 x 8192, 16 heads of 256 / 512: 128 blocks of four groups, 1,030 us, 8.1 us a
+// chunk; with one term of S, U and P for the outputs a sixth less (the helper's
+// products share the tensor pipe, and tiles of two terms leave the rings one stage
+// each).
+// 4 x 2047, 16 heads of 128 / 128: 163 us, 5.1 us a chunk of the longest sequence.
+// The backward's chains of 1 x 4096, 16 heads of 128 / 128: 64 blocks of two groups a
+// way, 300 us.
 #include <algorithm>
 
 #include "delta_util.cuh"
@@ -381,7 +387,7 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
         float m_own = tiles_max(S);
         uint8_t *xf = ex + Pl::oX, *ef = ex + Pl::oE;
         // R of quarter q, in its owner's part of the exchange of X: quarters 0, 3, 1, 2
-        auto rf = [&](int q) { return xf + (q == 0 ? 0 : q == 3 ? 1024 : q == 1 ? 2048 : 3072); };
+        auto rf = [&](int q) { return xf + 1024 * (q == 0 ? 0 : q == 3 ? 1 : q == 1 ? 2 : 3); };
         for (int c = 0; c < n_chunks; c++) {
             uint8_t* st = sh.sm + (c % NA) * Pl::A;
             const uint32_t sK = tc::smem_u32(st), sT = sK + Pl::oT;
@@ -467,7 +473,7 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
             float U[4][4];
             zero(U);
             // the small products, then the large ones; for the gradients in passes of
-            // their own (the forward at dk 256: 939 us with, 916 without)
+            // their own (which would cost the forward 2% at dk 256)
             constexpr int kPasses = MODE == kKeep ? 2 : 1;
 #pragma unroll
             for (int pass = 0; pass < kPasses; pass++)
@@ -722,7 +728,7 @@ __device__ __forceinline__ void chain_backward(const ChainArgs& a, const float* 
         float m_own = tiles_max(S);
         uint8_t *xf = ex + Pl::oX, *ef = ex + Pl::oE;
         // R of quarter q, in its owner's part of the exchange of X: quarters 0, 3, 1, 2
-        auto rf = [&](int q) { return xf + (q == 0 ? 0 : q == 3 ? 1024 : q == 1 ? 2048 : 3072); };
+        auto rf = [&](int q) { return xf + 1024 * (q == 0 ? 0 : q == 3 ? 1 : q == 1 ? 2 : 3); };
         for (int it = 0; it < n_chunks; it++) {
             uint8_t* st = sh.sm + (it % NA) * Pl::A;
             const uint32_t sK = tc::smem_u32(st), sT = sK + Pl::oT;

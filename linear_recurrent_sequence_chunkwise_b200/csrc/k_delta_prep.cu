@@ -10,8 +10,8 @@
 // tensor cores, a warp per block column.
 //
 // Bound by instruction issue and the barriers between its short phases: 1 x 8192,
-// 16 heads of 256: 137 us for 2,048 chunks and heads; 4 x 2047 (1,472 chunks and
-// heads of 128): 56 us with four blocks an SM, 66 us with three.
+// 16 heads of 256: 122 us for 2,048 chunks and heads; 4 x 2047 (1,472 chunks and
+// heads of 128): 50 us with four blocks an SM, a fifth more with three.
 #include "delta_util.cuh"
 
 namespace ret {
