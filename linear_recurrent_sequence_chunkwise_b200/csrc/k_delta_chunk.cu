@@ -605,15 +605,21 @@ __device__ __forceinline__ void chain_forward(const ChainArgs& a, int b) {
             zero(O);
             wait(sh.fb + c % NB, c / NB);
             wait(sh.s_ready + cg, c);
-            const float s0 = sh.s_inv[2 * cg], si = sh.s_inv[2 * cg + 1];
+            // The halves have their own scales.  The smaller one's goes first: its sums
+            // shrink to the larger one's units, where the other way round they could
+            // pass fp32's range.
+            const float s0 = sh.s_inv[2 * cg], s1 = sh.s_inv[2 * cg + 1], si = fmaxf(s0, s1);
+            const int first = s0 <= s1 ? 0 : KK / 2;
 #pragma unroll 4
-            for (int kk = 0; kk < KK; kk++) {
-                if (kk == KK / 2) {  // the halves have their own scales
+            for (int i = 0; i < KK; i++) {
+                if (i == KK / 2) {
+                    const float f = fminf(s0, s1) / si;
 #pragma unroll
                     for (int n = 0; n < 8; n++)
 #pragma unroll
-                        for (int e = 0; e < 4; e++) O[n][e] *= s0 / si;
+                        for (int e = 0; e < 4; e++) O[n][e] *= f;
                 }
+                const int kk = i ^ first;
                 uint32_t hi[4], lo[4];
                 get4(sf + kk * 512, hi, lane);
                 get4(sf + Pl::sHalf + kk * 512, lo, lane);

@@ -76,3 +76,23 @@ def test_the_final_state_behind_a_strong_decay(N, dk, dv, g, last):
     _, ref = od.delta_forward(**f64(f), initial_state=host64(s0))
     assert np.abs(ref).max() < 1e-3
     assert err_state(host64(S), ref) < TOL_SPLIT
+
+
+# Halves of a state's rows many powers of two apart: finite, and good to 2^-18 of the
+# output's norm, whichever half is the larger and whichever the queries read.
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("low,high", [(50, -85), (-85, 50), (0, -80), (-60, 60)])
+@pytest.mark.parametrize("dk", [64, 256])
+def test_halves_of_a_state_far_apart(dk, low, high, out_dtype):
+    B, N, H, dv = 1, 70, 2, 40
+    f, s0 = inputs(944, B, N, H, H, dk, dv, "bf16")
+    s0[:, :, :dk // 2] *= 2.0 ** low
+    s0[:, :, dk // 2:] *= 2.0 ** high
+    f["beta"].zero_()  # nothing written: a write would spread one half's size over the other
+    f["g"].zero_()
+    f["q"][:, :20, :, :dk // 2] = 0
+    f["q"][:, 20:40, :, dk // 2:] = 0
+    out, S = R.ret_delta_forward_chunkwise(**cuda(f), initial_state=s0.cuda(), out_dtype=out_dtype, want_final_state=True)
+    ref, _ = od.delta_forward(**f64(f), initial_state=host64(s0))
+    assert torch.equal(S.cpu(), s0) and torch.isfinite(out).all()
+    assert np.linalg.norm(host64(out) - ref) <= (TOL_SPLIT if out_dtype == torch.float32 else 2.0 ** -8) * np.linalg.norm(ref)
