@@ -30,7 +30,7 @@
 // chunk; with one term of S, U and P for the outputs a sixth less (the helper's
 // products share the tensor pipe, and tiles of two terms leave the rings one stage
 // each).
-// 4 x 2047, 16 heads of 128 / 128: 163 us, 5.1 us a chunk of the longest sequence.
+// 4 x 2047, 16 heads of 128 / 128: 166 us, 5.2 us a chunk of the longest sequence.
 // The backward's chains of 1 x 4096, 16 heads of 128 / 128: 64 blocks of two groups a
 // way, 300 us.
 #include <algorithm>
